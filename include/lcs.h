@@ -64,6 +64,12 @@ extern "C" {
                          §4: the indexer's QK path is FP4).  A tensor of n vectors of length d
                          is two planes: n*d/2 packed bytes (element 2j in the low nibble of
                          byte j), then n*d/32 scale bytes. */
+#define LCS_KV_FP4 4  /* 4-bit KV row ("DeepSeek V4 深度解析" §4, FP4; RoPE dims BF16 as in §2): for
+                         d_c content dims and d_r RoPE dims one row is d_c/2 bytes of E2M1 codes
+                         (element 2j in the low nibble of byte j) | d_r bf16 | d_c/32 E4M3 scales,
+                         scale b applying to content dims [32b, 32b+32), zero-padded to a multiple
+                         of 16 bytes.  d_c = 512, d_r = 64: 400 bytes.  The type of the paged pool
+                         that the lcs_kv4_* and *_attend_kv4 calls read and write. */
 
 /* ---- attention modes ---- */
 #define LCS_MODE_CSA 0
@@ -75,6 +81,7 @@ extern "C" {
 #define LCS_OP_DECODE     3
 #define LCS_OP_TOPK       4
 #define LCS_OP_CP_SELECT  5
+#define LCS_OP_ATTEND_KV4 6
 
 /*
  * Token compressor, CSA ("DeepSeek V4 深度解析" §2, CSA step 1; "V3 vs V4" page,
@@ -319,6 +326,86 @@ LCS_API int lcs_cache_append(int64_t B, const int64_t* pos, const void* x, const
                  int kv_dtype, int kI_dtype, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * The compressed cache in pages and 4 bits ("DeepSeek V4 深度解析" §4, KV-cache management:
+ * the compressed entries lie in blocks, each covering lcm(4, 128) raw tokens; FP4).  A pool
+ * holds n_blocks blocks of block_entries rows each; block_table[b][i] is the block of
+ * request b's entries [i*block_entries, (i+1)*block_entries), so entry e lies in slot
+ * block_table[b][e / block_entries] * block_entries + e % block_entries.  With blocks of 128
+ * tokens the CSA pool has 32 entries a block, the HCA pool one; one table serves both.
+ *
+ * lcs_page_plan: the block tables and slots for the tokens that the requests are about to
+ * append.  Request b holds len[b] tokens and gets n_new[b] (<= 0: none; len < 0: none).
+ *   - its blocks [ceil(len/P), ceil((len+n_new)/P)), P = block_tokens, are taken from
+ *     free_blocks [n_free] in order, request by request, and written into block_table
+ *     [B, max_blocks]; other table entries are left as they are.  taken [1] is their number:
+ *     the free list goes on at free_blocks + taken;
+ *   - slots [max_slots] gets the slots of the entries of m tokens that complete, entries
+ *     [len/m, (len+n_new)/m) of request 0, then of request 1, ...; -1 behind the last.
+ *     offsets [B+1]: request b's are slots[offsets[b] .. offsets[b+1]).  slots2, max_slots2,
+ *     offsets2: the same for entries of m2 tokens (m2 = 0: left out, the pointers may be
+ *     NULL).  P is a multiple of m and m2.
+ * When n_free blocks, max_blocks table entries or max_slots slots do not suffice, nothing is
+ * taken: LCS_ERR_DEVICE goes to the status word of ws, the table stays as it is, taken and
+ * offsets are 0 and the slots -1.  B <= 8192.  All arrays on the device; ws >= 256 bytes.
+ */
+LCS_API int lcs_page_plan(int64_t B, const int64_t* len, const int64_t* n_new, int block_tokens,
+                 const int32_t* free_blocks, int64_t n_free, int32_t* block_table, int64_t max_blocks, int m,
+                 int64_t* slots, int64_t max_slots, int64_t* offsets, int m2, int64_t* slots2, int64_t max_slots2,
+                 int64_t* offsets2, int64_t* taken, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * lcs_kv4_store: quantises rows and stores them in a pool of LCS_KV_FP4 rows: row i of
+ * x [n, d_c + d_r] (LCS_F32 or LCS_BF16) goes to slot slots[i] (int64); slots[i] < 0 stores
+ * nothing.  Per block of 32 content dims: scale = E4M3(amax/6) (1 when that is 0), code =
+ * E2M1(x/scale), as lcs_quant_fp4; values past 6 * 448 saturate, a NaN element is stored as
+ * some finite value; RoPE dims rounded to bf16.  The slots of one call are distinct (rows that
+ * share one leave a mixture of them there).
+ * lcs_kv4_load: the values of stored rows: out [n, d_c + d_r] (LCS_F32 or LCS_BF16, both
+ * exact) from slots[i]; slots[i] < 0 gives a row of zeros.
+ * pool [n_slots, row] with n_slots = n_blocks * block_entries.  A slot >= n_slots is not
+ * written (read as zeros) and records LCS_ERR_DEVICE in the status word of ws (>= 256
+ * bytes).  d_c % 32 == 0, d_c <= 512, d_r % 8 == 0, d_r <= 128; x, pool and out on 16 bytes.
+ */
+LCS_API int lcs_kv4_store(const void* x, int x_dtype, int64_t n, int d_c, int d_r, const int64_t* slots, void* pool,
+                 int64_t n_slots, void* ws, size_t ws_bytes, cudaStream_t stream);
+LCS_API int lcs_kv4_load(const void* pool, int64_t n_slots, const int64_t* slots, int64_t n, int d_c, int d_r, void* out,
+                 int out_dtype, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * CSA sparse and HCA dense attention over the paged 4-bit cache: csa_attend and hca_attend
+ * with the compressed rows in a pool of LCS_KV_FP4 rows and the window rows in q's type.
+ *   q    [B, Q, H, d_c + d_r]  LCS_F32 or LCS_BF16, 1 <= H <= 128
+ *   pool [n_blocks, block_entries, row], block_table [B, max_blocks] int32
+ *   n_entries [B] int64   the entries that request b has (any length, 0 included)
+ *   win  [B, Tw, d_c + d_r]  q's type (NULL when Tw is 0)
+ *   n_win [B] int64 or NULL  decode: request b's window is win[b][0 .. n_win[b]) (NULL: all Tw
+ *        rows); a ring buffer of 128 slots has min(tokens, 128).  NULL when q_pos is not.
+ *   CSA: idx [B, Q, k] int32, k <= 4096: valid entries first, then -1 padding; the first -1 ends
+ *        the selection.  An index >= n_entries[b] also ends it and records LCS_ERR_DEVICE.
+ *   HCA: every entry of the request (decode), or those below (q_pos + 1) / m.
+ *   q_pos [B, Q], win_pos0 [B], W: as csa_attend; both NULL for decode (Q = 1)
+ *   out  [B, Q, H, d_c]  LCS_F32 or LCS_BF16;  lse [B, Q, H] fp32 or NULL
+ * V is the d_c content dims.  A query that sees no row gives o = 0 and lse = -inf.  Only
+ * blocks of rows that are attended are looked up: table entries behind a request's last
+ * block and rows behind its last entry may hold anything.  A block id outside [0, n_blocks)
+ * records LCS_ERR_DEVICE and leaves that query's output unspecified; n_entries past
+ * max_blocks * block_entries records it too and counts as that.
+ * d_c, d_r as lcs_kv4_store; d_c = 512, d_r = 64 with bf16 q runs on the tensor cores.  q,
+ * pool, win and out on 16 bytes.  Workspace: lcs_workspace_size(LCS_OP_ATTEND_KV4, B, Q, N_c =
+ * max_blocks * block_entries, Tw, k (0 for HCA), H, d_v = d_c, 0).
+ */
+LCS_API int csa_attend_kv4(const void* q, int q_dtype, const void* pool, int64_t n_blocks, int block_entries,
+                 const int32_t* block_table, int64_t max_blocks, const int64_t* n_entries, const void* win,
+                 const int64_t* n_win, int64_t B, int64_t Q, int64_t Tw, const int32_t* idx, int k,
+                 const int64_t* q_pos, const int64_t* win_pos0, int W, int H, int d_c, int d_r, float scale,
+                 void* out, int out_dtype, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+LCS_API int hca_attend_kv4(const void* q, int q_dtype, const void* pool, int64_t n_blocks, int block_entries,
+                 const int32_t* block_table, int64_t max_blocks, const int64_t* n_entries, const void* win,
+                 const int64_t* n_win, int64_t B, int64_t Q, int64_t Tw, const int64_t* q_pos,
+                 const int64_t* win_pos0, int m, int W, int H, int d_c, int d_r, float scale, void* out,
+                 int out_dtype, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * Context parallelism for long requests: the compressed entries (and index keys) of every
  * request are split over G ranks, rank r holding the S entries [offset, offset + S).  One
  * decode step is, on every rank: csa_index_topk over the rank's entries (local top-k, local
@@ -390,6 +477,7 @@ LCS_API int lcs_quant_fp4(const float* x, int64_t n, int d, void* out, cudaStrea
  *   LCS_OP_INDEX_TOPK: B, Q, N_c, k, score_dtype     LCS_OP_TOPK: B, Q, N_c, k
  *   LCS_OP_ATTEND: B, Q, H, d_v (+ N_c, Tw, k for the split plan)
  *   LCS_OP_CP_SELECT: B, Q = G (ranks), k
+ *   LCS_OP_ATTEND_KV4: B, Q, N_c = max_blocks * block_entries, Tw, k, H, d_v = d_c
  *   LCS_OP_DECODE: everything (both stages)
  * Returns a negative value for invalid sizes.  The first 256 bytes hold the
  * status word; the workspace must be 256-byte aligned.

@@ -13,15 +13,15 @@ import ctypes as C
 import os
 
 __all__ = [
-    "F32", "BF16", "KV_FP8", "FP4", "MODE_CSA", "MODE_HCA", "LcsError", "lib",
+    "F32", "BF16", "KV_FP8", "FP4", "KV_FP4", "MODE_CSA", "MODE_HCA", "LcsError", "lib",
     "csa_compress", "hca_compress", "lcs_compress_proj", "csa_index_topk", "csa_index_topk_proj", "lcs_topk", "csa_attend", "hca_attend",
-    "decode_fused", "lcs_cache_append", "lcs_cp_candidates", "lcs_cp_select", "lcs_attn_merge", "group_oproj", "lcs_rope", "lcs_quant_kv_fp8", "lcs_quant_fp4",
+    "decode_fused", "lcs_cache_append", "lcs_cp_candidates", "lcs_cp_select", "lcs_attn_merge", "lcs_page_plan", "lcs_kv4_store", "lcs_kv4_load", "csa_attend_kv4", "hca_attend_kv4", "kv_fp4_row_bytes", "group_oproj", "lcs_rope", "lcs_quant_kv_fp8", "lcs_quant_fp4",
     "lcs_workspace_size", "lcs_status", "lcs_clear_status", "lcs_selftest_wait", "workspace", "kv_fp8_row_bytes",
 ]
 
-F32, BF16, KV_FP8, FP4 = 0, 1, 2, 3
+F32, BF16, KV_FP8, FP4, KV_FP4 = 0, 1, 2, 3, 4
 MODE_CSA, MODE_HCA = 0, 1
-OP_INDEX_TOPK, OP_ATTEND, OP_DECODE, OP_TOPK, OP_CP_SELECT = 1, 2, 3, 4, 5
+OP_INDEX_TOPK, OP_ATTEND, OP_DECODE, OP_TOPK, OP_CP_SELECT, OP_ATTEND_KV4 = 1, 2, 3, 4, 5, 6
 # return codes (include/lcs.h)
 LCS_OK, LCS_ERR_INVALID, LCS_ERR_UNSUPPORTED, LCS_ERR_CUDA = 0, -1, -2, -3
 LCS_ERR_TIMEOUT, LCS_ERR_DEVICE, LCS_ERR_WORKSPACE, LCS_ERR_TOO_LARGE = -4, -5, -6, -7
@@ -61,6 +61,12 @@ def lib():
             "csa_index_topk_proj": [P, I, P, P, P, I64, I64, I64, I, I, P, I, I, P, P, P, SZ, P],
             "lcs_cp_select": [P, P, I, I64, I, I64, I64, P, P, P, SZ, P],
             "lcs_attn_merge": [P, P, I, I64, I, P, I, P, P],
+            "lcs_page_plan": [I64, P, P, I, P, I64, P, I64, I, P, I64, P, I, P, I64, P, P, P, SZ, P],
+            "lcs_kv4_store": [P, I, I64, I, I, P, P, I64, P, SZ, P],
+            "lcs_kv4_load": [P, I64, P, I64, I, I, P, I, P, SZ, P],
+            "csa_attend_kv4": [P, I, P, I64, I, P, I64, P, P, P, I64, I64, I64, P, I, P, P, I, I, I, I, F, P, I, P, P, SZ,
+                               P],
+            "hca_attend_kv4": [P, I, P, I64, I, P, I64, P, P, P, I64, I64, I64, P, P, I, I, I, I, I, F, P, I, P, P, SZ, P],
             "decode_fused": [I, I64, P, I, P, P, I, I64, I64, I, I, I, F, P, I, P, P, I, I, I, I, I, P, I, P, P, P,
                              SZ, P],
             "group_oproj": [P, I64, I, I, P, I, I, P, I, P, P],
@@ -356,6 +362,144 @@ def lcs_cache_append(pos, x, kx, z, zI, zh, bias, biasI, biash, raw, logits, win
           _ptr(comp), _ptr(kI), _ptr(hca), N_c, hca.shape[1], kv_dtype, kI_dtype, _ptr(ws), ws.numel(),
           _stream(stream))
     return ws
+
+
+# ------------------------------------------------- paged compressed cache in 4 bits
+def kv_fp4_row_bytes(d_c=512, d_r=64):
+    return (d_c // 2 + 2 * d_r + d_c // 32 + 15) // 16 * 16
+
+
+def _need(t, name, dtype, shape=None, like=None):
+    """Checks one argument of a paged-cache call (the C call sees addresses only)."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {shape} expected, got {tuple(t.shape)}")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, the other tensors on {like.device}")
+
+
+def _call_on(t, name, stream, *args):
+    """The call on t's device: with that device current, on `stream` or its current stream."""
+    torch = _torch()
+    if t.device.index == torch.cuda.current_device():
+        return _call(name, *args, _stream(stream))
+    with torch.cuda.device(t.device):
+        return _call(name, *args, _stream(stream))
+
+
+def lcs_page_plan(lens, n_new, free_blocks, block_table, block_tokens=128, m=4, max_slots=0, m2=0, max_slots2=0,
+                  ws=None, stream=None):
+    """lens, n_new [B] int64; free_blocks [n_free] int32; block_table [B, max_blocks] int32, extended in
+    place -> (slots [max_slots], offsets [B+1], slots2 [max_slots2], offsets2 [B+1], taken [1]), int64;
+    slots2 and offsets2 are None when m2 is 0."""
+    torch = _torch()
+    i64 = torch.int64
+    B = lens.shape[0]
+    _need(lens, "lens", i64, (B,))
+    _need(n_new, "n_new", i64, (B,), lens)
+    _need(free_blocks, "free_blocks", torch.int32, (free_blocks.numel(),), lens)
+    _need(block_table, "block_table", torch.int32, (B, block_table.shape[-1]), lens)
+    dev = lens.device
+    slots = torch.empty(max_slots, dtype=i64, device=dev)
+    off = torch.empty(B + 1, dtype=i64, device=dev)
+    slots2 = torch.empty(max_slots2, dtype=i64, device=dev) if m2 else None
+    off2 = torch.empty(B + 1, dtype=i64, device=dev) if m2 else None
+    taken = torch.empty(1, dtype=i64, device=dev)
+    if ws is None:
+        ws = workspace(256, dev)
+    _call_on(lens, "lcs_page_plan", stream, B, _ptr(lens), _ptr(n_new), block_tokens, _ptr(free_blocks),
+             free_blocks.numel(), _ptr(block_table), block_table.shape[1], m, _ptr(slots), max_slots, _ptr(off), m2,
+             _ptr(slots2), max_slots2 if m2 else 0, _ptr(off2), _ptr(taken), _ptr(ws), ws.numel())
+    return slots, off, slots2, off2, taken
+
+
+def _pool_slots(pool, d_c, d_r, like):
+    """Slots of a pool [n_blocks, block_entries, row] (or [n_slots, row]) of 4-bit rows."""
+    _need(pool, "pool", _torch().uint8, tuple(pool.shape[:-1]) + (kv_fp4_row_bytes(d_c, d_r),), like)
+    n = 1
+    for s in pool.shape[:-1]:
+        n *= s
+    return n
+
+
+def lcs_kv4_store(x, slots, pool, d_c=512, ws=None, stream=None):
+    """Quantises x [n, d_c + d_r] (fp32/bf16) into the pool's 4-bit rows at slots [n] int64 (negative: skipped)."""
+    n, D = x.shape
+    _need(slots, "slots", _torch().int64, (n,), x)
+    n_slots = _pool_slots(pool, d_c, D - d_c, x)
+    if ws is None:
+        ws = workspace(256, x.device)
+    _call_on(x, "lcs_kv4_store", stream, _ptr(x), _dt(x), n, d_c, D - d_c, _ptr(slots), _ptr(pool), n_slots, _ptr(ws),
+             ws.numel())
+    return pool
+
+
+def lcs_kv4_load(pool, slots, d_c=512, d_r=64, out_dtype=None, out=None, ws=None, stream=None):
+    """The values of the pool's rows at slots [n] int64 (negative: zeros) -> [n, d_c + d_r] (bf16 or fp32)."""
+    torch = _torch()
+    _need(slots, "slots", torch.int64, (slots.numel(),), pool)
+    n_slots = _pool_slots(pool, d_c, d_r, pool)
+    n = slots.shape[0]
+    if out is None:
+        out = torch.empty((n, d_c + d_r), dtype=out_dtype or torch.bfloat16, device=pool.device)
+    else:
+        _need(out, "out", out_dtype or out.dtype, (n, d_c + d_r), pool)
+    if ws is None:
+        ws = workspace(256, pool.device)
+    _call_on(pool, "lcs_kv4_load", stream, _ptr(pool), n_slots, _ptr(slots), n, d_c, d_r, _ptr(out), _dt(out), _ptr(ws),
+             ws.numel())
+    return out
+
+
+def _attend_kv4(name, q, pool, block_table, n_entries, win, idx, k, hca_m, scale, d_c, n_win, q_pos, win_pos0, W,
+                want_lse, out_dtype, ws, stream):
+    torch = _torch()
+    B, Q, H, D = q.shape
+    _need(pool, "pool", torch.uint8, tuple(pool.shape[:2]) + (kv_fp4_row_bytes(d_c, D - d_c),), q)
+    n_blocks, be, _ = pool.shape
+    max_blocks = block_table.shape[1]
+    _need(block_table, "block_table", torch.int32, (B, max_blocks), q)
+    _need(n_entries, "n_entries", torch.int64, (B,), q)
+    Tw = 0
+    if win is not None:
+        Tw = win.shape[1]
+        _need(win, "win", q.dtype, (B, Tw, D), q)
+    if n_win is not None:
+        _need(n_win, "n_win", torch.int64, (B,), q)
+    if q_pos is not None:
+        _need(q_pos, "q_pos", torch.int64, (B, Q), q)
+    if win_pos0 is not None:
+        _need(win_pos0, "win_pos0", torch.int64, (B,), q)
+    if idx is not None:
+        _need(idx, "idx", torch.int32, (B, Q, k), q)
+    out = torch.empty((B, Q, H, d_c), dtype=out_dtype or q.dtype, device=q.device)
+    lse = torch.empty((B, Q, H), dtype=torch.float32, device=q.device) if want_lse else None
+    if ws is None:
+        ws = workspace(lcs_workspace_size(OP_ATTEND_KV4, B, Q, max_blocks * be, Tw, k, H, d_c), q.device)
+    tail = (W, H, d_c, D - d_c, scale, _ptr(out), _dt(out), _ptr(lse), _ptr(ws), ws.numel())
+    head = (_ptr(q), _dt(q), _ptr(pool), n_blocks, be, _ptr(block_table), max_blocks, _ptr(n_entries), _ptr(win),
+            _ptr(n_win), B, Q, Tw)
+    if hca_m is None:
+        _call_on(q, name, stream, *head, _ptr(idx), k, _ptr(q_pos), _ptr(win_pos0), *tail)
+    else:
+        _call_on(q, name, stream, *head, _ptr(q_pos), _ptr(win_pos0), hca_m, *tail)
+    return (out, lse) if want_lse else out
+
+
+def csa_attend_kv4(q, pool, block_table, n_entries, win, idx, scale, d_c=512, n_win=None, q_pos=None, win_pos0=None,
+                   W=128, want_lse=False, out_dtype=None, ws=None, stream=None):
+    """q [B,Q,H,D] (fp32/bf16); pool [n_blocks,block_entries,row] uint8; block_table [B,max_blocks] int32;
+    n_entries [B] int64; win [B,Tw,D] in q's type or None; idx [B,Q,k] int32 -> out [B,Q,H,d_c] (and lse)."""
+    return _attend_kv4("csa_attend_kv4", q, pool, block_table, n_entries, win, idx, idx.shape[-1], None, scale, d_c,
+                       n_win, q_pos, win_pos0, W, want_lse, out_dtype, ws, stream)
+
+
+def hca_attend_kv4(q, pool, block_table, n_entries, win, scale, d_c=512, n_win=None, q_pos=None, win_pos0=None, m=128,
+                   W=128, want_lse=False, out_dtype=None, ws=None, stream=None):
+    """As csa_attend_kv4 over every entry of the request (with q_pos: those below (q_pos + 1) / m)."""
+    return _attend_kv4("hca_attend_kv4", q, pool, block_table, n_entries, win, None, 0, m, scale, d_c, n_win, q_pos,
+                       win_pos0, W, want_lse, out_dtype, ws, stream)
 
 
 # ------------------------------------------------- context parallelism (one long request)

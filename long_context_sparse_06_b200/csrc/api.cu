@@ -130,6 +130,29 @@ cudaError_t set_smem_once(const void* kern, size_t bytes) {
     return cudaSuccess;
 }
 
+cudaError_t set_smem_here(const void* kern, size_t bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;   // allowed without the attribute
+    struct Slot {
+        const void* kern;
+        int dev;
+        size_t bytes;
+    };
+    static Slot slots[kAttrSlots];
+    static int n = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_attr_mutex);
+    int i = 0;
+    while (i < n && !(slots[i].kern == kern && slots[i].dev == dev)) ++i;
+    if (i < n && slots[i].bytes >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    if (i < kAttrSlots) slots[i] = Slot{kern, dev, bytes};
+    if (i == n && n < kAttrSlots) ++n;
+    return cudaSuccess;
+}
+
 bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz) {
     const TmapKey key{(int)dt, base, inner, outer, row_stride_bytes, box_inner, box_outer, (int)swz};
@@ -509,6 +532,109 @@ int decode_fused(int mode, int64_t B, const void* q, int q_dtype, const void* co
     return LCS_OK;
 }
 
+// ------------------------------------------------- paged compressed cache in 4 bits
+static bool kv4_dims_ok(int d_c, int d_r) {
+    return d_c > 0 && d_c <= 512 && d_c % 32 == 0 && d_r >= 0 && d_r <= 128 && d_r % 8 == 0;
+}
+
+static bool bad_ws(const void* ws, size_t ws_bytes, int64_t need) {
+    return ws == nullptr || (int64_t)ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255);
+}
+
+int lcs_page_plan(int64_t B, const int64_t* len, const int64_t* n_new, int block_tokens, const int32_t* free_blocks,
+                  int64_t n_free, int32_t* block_table, int64_t max_blocks, int m, int64_t* slots, int64_t max_slots,
+                  int64_t* offsets, int m2, int64_t* slots2, int64_t max_slots2, int64_t* offsets2, int64_t* taken,
+                  void* ws, size_t ws_bytes, cudaStream_t stream) {
+    if (offsets == nullptr || taken == nullptr || (m2 != 0 && offsets2 == nullptr)) return LCS_ERR_INVALID;
+    if (B < 0 || n_free < 0 || max_blocks < 0 || max_slots < 0 || max_slots2 < 0) return LCS_ERR_INVALID;
+    if (B > 0 && (len == nullptr || n_new == nullptr)) return LCS_ERR_INVALID;
+    if ((n_free > 0 && free_blocks == nullptr) || (B * max_blocks > 0 && block_table == nullptr) ||
+        (max_slots > 0 && slots == nullptr) || (m2 != 0 && max_slots2 > 0 && slots2 == nullptr))
+        return LCS_ERR_INVALID;
+    if (block_tokens < 1 || block_tokens > (1 << 20) || m < 1 || block_tokens % m || m2 < 0 ||
+        (m2 > 0 && block_tokens % m2))
+        return LCS_ERR_INVALID;
+    if (B > page_plan_max_requests() || n_free >= (int64_t(1) << 31) || max_blocks >= (int64_t(1) << 31) ||
+        max_slots >= (int64_t(1) << 31) || max_slots2 >= (int64_t(1) << 31))
+        return LCS_ERR_UNSUPPORTED;
+    if (bad_ws(ws, ws_bytes, kStatusBytes)) return LCS_ERR_WORKSPACE;
+    if (!device_ok()) return LCS_ERR_CUDA;
+    return from_cuda(launch_page_plan(B, len, n_new, block_tokens, free_blocks, n_free, block_table, max_blocks, m,
+                                      slots, max_slots, offsets, m2, slots2, max_slots2, offsets2, taken,
+                                      status_of(ws), stream));
+}
+
+int lcs_kv4_store(const void* x, int x_dtype, int64_t n, int d_c, int d_r, const int64_t* slots, void* pool,
+                  int64_t n_slots, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    if (n < 0 || n_slots < 0 || !kv4_dims_ok(d_c, d_r)) return LCS_ERR_INVALID;
+    if (x_dtype != LCS_F32 && x_dtype != LCS_BF16) return LCS_ERR_UNSUPPORTED;
+    if (n > 0 && (x == nullptr || slots == nullptr)) return LCS_ERR_INVALID;
+    if (n > 0 && n_slots > 0 && pool == nullptr) return LCS_ERR_INVALID;
+    if (!aligned16(x) || !aligned16(pool)) return LCS_ERR_INVALID;
+    if (bad_ws(ws, ws_bytes, kStatusBytes)) return LCS_ERR_WORKSPACE;
+    if (!device_ok()) return LCS_ERR_CUDA;
+    return from_cuda(launch_kv4_store(x, x_dtype, n, d_c, d_r, slots, pool, n_slots, status_of(ws), stream));
+}
+
+int lcs_kv4_load(const void* pool, int64_t n_slots, const int64_t* slots, int64_t n, int d_c, int d_r, void* out,
+                 int out_dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    if (n < 0 || n_slots < 0 || !kv4_dims_ok(d_c, d_r)) return LCS_ERR_INVALID;
+    if (out_dtype != LCS_F32 && out_dtype != LCS_BF16) return LCS_ERR_UNSUPPORTED;
+    if (n > 0 && (out == nullptr || slots == nullptr)) return LCS_ERR_INVALID;
+    if (n > 0 && n_slots > 0 && pool == nullptr) return LCS_ERR_INVALID;
+    if (!aligned16(out) || !aligned16(pool)) return LCS_ERR_INVALID;
+    if (bad_ws(ws, ws_bytes, kStatusBytes)) return LCS_ERR_WORKSPACE;
+    if (!device_ok()) return LCS_ERR_CUDA;
+    return from_cuda(launch_kv4_load(pool, n_slots, slots, n, d_c, d_r, out, out_dtype, status_of(ws), stream));
+}
+
+static int run_attend_kv4(const AttendKv4Args& a, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    if (a.B < 0 || a.Q < 0 || a.n_blocks < 0 || a.max_blocks < 0 || a.Tw < 0 || a.be < 1 || a.be > (1 << 20) ||
+        a.W < 1 || a.m < 1 || a.H < 1 || !kv4_dims_ok(a.d_c, a.d_r))
+        return LCS_ERR_INVALID;
+    if (a.H > 128) return LCS_ERR_UNSUPPORTED;
+    if (a.q_dtype != LCS_F32 && a.q_dtype != LCS_BF16) return LCS_ERR_UNSUPPORTED;
+    if (a.out_dtype != LCS_F32 && a.out_dtype != LCS_BF16) return LCS_ERR_UNSUPPORTED;
+    if (a.B * a.Q > 0 && (a.q == nullptr || a.out == nullptr || a.n_entries == nullptr)) return LCS_ERR_INVALID;
+    if (a.B * a.Q > 0 && a.B * a.max_blocks > 0 && (a.table == nullptr || a.pool == nullptr)) return LCS_ERR_INVALID;
+    if (a.B * a.Q > 0 && a.Tw > 0 && a.win == nullptr) return LCS_ERR_INVALID;
+    if ((a.q_pos == nullptr) != (a.win_pos0 == nullptr)) return LCS_ERR_INVALID;
+    if (a.q_pos == nullptr && a.Q != 1) return LCS_ERR_INVALID;
+    if (a.q_pos != nullptr && a.n_win != nullptr) return LCS_ERR_INVALID;
+    if (!aligned16(a.q) || !aligned16(a.pool) || !aligned16(a.win) || !aligned16(a.out)) return LCS_ERR_INVALID;
+    if (a.max_blocks >= (int64_t(1) << 31) / a.be || a.B >= (int64_t(1) << 24) || a.Q >= (int64_t(1) << 31) ||
+        a.B * a.Q * 2 >= (int64_t(1) << 31) || a.Tw >= (int64_t(1) << 31) || a.n_blocks >= (int64_t(1) << 31))
+        return LCS_ERR_UNSUPPORTED;
+    if (bad_ws(ws, ws_bytes, kStatusBytes + attend_kv4_scratch_bytes(a))) return LCS_ERR_WORKSPACE;
+    if (!device_ok()) return LCS_ERR_CUDA;
+    return from_cuda(launch_attend_kv4(a, static_cast<uint8_t*>(ws) + kStatusBytes, status_of(ws), stream));
+}
+
+int csa_attend_kv4(const void* q, int q_dtype, const void* pool, int64_t n_blocks, int block_entries,
+                   const int32_t* block_table, int64_t max_blocks, const int64_t* n_entries, const void* win,
+                   const int64_t* n_win, int64_t B, int64_t Q, int64_t Tw, const int32_t* idx, int k,
+                   const int64_t* q_pos, const int64_t* win_pos0, int W, int H, int d_c, int d_r, float scale,
+                   void* out, int out_dtype, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    if (k < 0 || k > 4096 || (k > 0 && B * Q > 0 && idx == nullptr)) return LCS_ERR_INVALID;
+    // an empty selection still is one: k = 0 attends the window alone
+    const int32_t* sel = idx != nullptr ? idx : reinterpret_cast<const int32_t*>(n_entries);
+    AttendKv4Args a{q, static_cast<const uint8_t*>(pool), block_table, n_entries, win, n_win, sel, q_pos, win_pos0,
+                    B, Q, n_blocks, max_blocks, Tw, block_entries, k, 1, W, H, d_c, d_r, kv4_row_bytes(d_c, d_r),
+                    q_dtype, out_dtype, scale, out, lse};
+    return run_attend_kv4(a, ws, ws_bytes, stream);
+}
+
+int hca_attend_kv4(const void* q, int q_dtype, const void* pool, int64_t n_blocks, int block_entries,
+                   const int32_t* block_table, int64_t max_blocks, const int64_t* n_entries, const void* win,
+                   const int64_t* n_win, int64_t B, int64_t Q, int64_t Tw, const int64_t* q_pos,
+                   const int64_t* win_pos0, int m, int W, int H, int d_c, int d_r, float scale, void* out,
+                   int out_dtype, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    AttendKv4Args a{q, static_cast<const uint8_t*>(pool), block_table, n_entries, win, n_win, nullptr, q_pos, win_pos0,
+                    B, Q, n_blocks, max_blocks, Tw, block_entries, 0, m, W, H, d_c, d_r, kv4_row_bytes(d_c, d_r),
+                    q_dtype, out_dtype, scale, out, lse};
+    return run_attend_kv4(a, ws, ws_bytes, stream);
+}
+
 // ------------------------------------------------------- decode cache update
 int lcs_cache_append(int64_t B, const int64_t* pos, const void* x, const void* kx, int x_dtype, const float* z,
                      const float* zI, const float* zh, const float* bias, const float* biasI, const float* biash,
@@ -630,6 +756,18 @@ int64_t lcs_workspace_size(int op, int64_t B, int64_t Q, int64_t N_c, int64_t Tw
             int64_t csa = decode_layout(LCS_MODE_CSA, B, N_c, Tw, k, score_dtype, score_dtype == LCS_BF16, &so, &io,
                                         &ao, c);
             return hca > csa ? hca : csa;
+        }
+        case LCS_OP_ATTEND_KV4: {
+            // Upper bound over CSA (k rows) and HCA (N_c rows) and over the types of q.
+            if (H < 1 || d_v < 1) return -1;
+            AttendKv4Args a{};
+            a.B = B, a.Q = Q, a.max_blocks = N_c, a.be = 1, a.Tw = Tw, a.H = H, a.W = 1 << 30;
+            a.d_c = d_v, a.d_r = 64, a.q_dtype = LCS_BF16;
+            AttendKv4Args c = a;
+            c.k = k;
+            c.idx = reinterpret_cast<const int32_t*>(1);
+            const int64_t s1 = attend_kv4_scratch_bytes(a), s2 = attend_kv4_scratch_bytes(c);
+            return kStatusBytes + align256(s1 > s2 ? s1 : s2);
         }
         default: return -1;
     }

@@ -400,6 +400,12 @@ __device__ __forceinline__ uint8_t f32_to_e2m1(float x) {
     return (uint8_t)__nv_cvt_float_to_fp4(x, __NV_E2M1, cudaRoundNearest) & 0xF;
 }
 
+// Two E2M1 codes (low nibble first) -> two floats.
+__device__ __forceinline__ float2 e2m1x2_to_f32(uint32_t byte) {
+    __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(byte & 0xFFu), __NV_E2M1);
+    return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
 // Order-preserving keys: larger float -> larger unsigned key; -0 maps like +0.
 __device__ __forceinline__ uint32_t f32_key(float f) {
     uint32_t u = __float_as_uint(f);

@@ -76,6 +76,40 @@ cudaError_t launch_cache_append(const int64_t* pos, const void* x, const void* k
                                 float* logits, void* win, int win_dtype, void* comp, void* kI, void* hca, int64_t B,
                                 int64_t N_c, int64_t N_h, int kv_dtype, int kI_dtype, int* status, cudaStream_t s);
 
+// paged.cu -- block tables, slot maps and the 4-bit rows of the paged compressed cache
+// Bytes of an LCS_KV_FP4 row: packed codes, bf16 RoPE dims, scales, padded to 16.
+inline int kv4_row_bytes(int d_c, int d_r) { return (d_c / 2 + 2 * d_r + d_c / 32 + 15) / 16 * 16; }
+int page_plan_max_requests();
+cudaError_t launch_page_plan(int64_t B, const int64_t* len, const int64_t* n_new, int block_tokens,
+                             const int32_t* free_blocks, int64_t n_free, int32_t* table, int64_t max_blocks, int m,
+                             int64_t* slots, int64_t max_slots, int64_t* off, int m2, int64_t* slots2,
+                             int64_t max_slots2, int64_t* off2, int64_t* taken, int* status, cudaStream_t s);
+cudaError_t launch_kv4_store(const void* x, int x_dtype, int64_t n, int d_c, int d_r, const int64_t* slots, void* pool,
+                             int64_t n_slots, int* status, cudaStream_t s);
+cudaError_t launch_kv4_load(const void* pool, int64_t n_slots, const int64_t* slots, int64_t n, int d_c, int d_r,
+                            void* out, int out_dtype, int* status, cudaStream_t s);
+
+// attend_kv4.cu -- shared-KV MQA over the paged 4-bit cache
+struct AttendKv4Args {
+    const void* q;
+    const uint8_t* pool;
+    const int32_t* table;
+    const int64_t* n_entries;
+    const void* win;          // [B, Tw, d_c + d_r] in q's type
+    const int64_t* n_win;     // valid window rows per request (decode) or nullptr
+    const int32_t* idx;       // CSA selection or nullptr (HCA)
+    const int64_t* q_pos;
+    const int64_t* win_pos0;
+    int64_t B, Q, n_blocks, max_blocks, Tw;
+    int be, k, m, W, H, d_c, d_r, row_bytes;
+    int q_dtype, out_dtype;
+    float scale;
+    void* out;
+    float* lse;
+};
+int64_t attend_kv4_scratch_bytes(const AttendKv4Args& a);
+cudaError_t launch_attend_kv4(const AttendKv4Args& a, void* scratch, int* status, cudaStream_t s);
+
 // cp.cu -- context parallelism for one long request (entries split over ranks)
 cudaError_t launch_cp_candidates(const void* scores, int score_dtype, int64_t B, int64_t S, const int32_t* idx_local,
                                  int k, int64_t offset, float* cand_score, int32_t* cand_idx, cudaStream_t s);
@@ -102,6 +136,10 @@ int noalloc_scratch(void** ptr);
 // Raises a kernel's dynamic shared-memory limit once per process and kernel (the
 // attribute call costs host time on every launch otherwise).
 cudaError_t set_smem_once(const void* kern, size_t bytes);
+
+// The same limit for kernels that run on any of the process's devices: the attribute
+// belongs to a device, so it is kept per kernel and device.
+cudaError_t set_smem_here(const void* kern, size_t bytes);
 
 // Launch helper with optional programmatic dependent launch.
 template <typename... KArgs, typename... Args>
