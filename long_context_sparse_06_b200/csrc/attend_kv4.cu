@@ -193,13 +193,782 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
     }
 }
 
+// ----------------------------------------------------------- tensor-core path
+// bf16 queries, d_c = 512, d_r = 64.  One CTA (448 threads) per (query, tile of 64 heads, split of
+// its row list); the row list is the window rows, padded to whole chunks of 64, then the selected
+// or available entries; chunk i goes to split i mod splits.
+//
+//   S [64 heads x 64 rows] = Q [64 x 576] . K_chunk^T,  O [64 x 512] += P [64 x 64] . V_chunk
+//
+// on tcgen05.mma with the heads as M = 64 (fp32 accumulators in TMEM: O as two interleaved M = 64
+// accumulators in columns 0-255, S double-buffered in 256-383).
+//
+//  * Widening.  code x scale has at most six significant bits and lies in [2^-10, 2688], so it is
+//    exact in fp16: one conversion per pair of codes and one fp16 multiply by the scale, half of what
+//    bf16 would take.  Both operands of a kind::f16 MMA have one type, so for these chunks the
+//    content dims of Q are fp16 too, scaled per head by a power of two that puts the head's largest
+//    element in [2^14, 2^15) (exact down to 2^-28 of it, below that off by 2^-39 of it), and P is fp16
+//    (11 bits; 2^-11 a weight, against 2^-8 of bf16).  RoPE dims stay bf16: four MMAs of the same
+//    accumulation.  Window rows are bf16 of any size: their chunks come first, with all of Q in
+//    bf16 (scaled by the same powers of two) and P in bf16; Q's content is then converted in place.
+//  * A chunk's 64 widened rows (72 KB) are the K-major B of Q.K^T and the MN-major B of P.V;
+//    two stages, each released in two halves of the columns as P.V leaves them.  Warps 4-11
+//    fill: a warp owns 8 rows and holds the next chunk's 400-byte rows in registers (six 16-byte loads
+//    a lane) while it waits for its stage; eight lanes take one row's 128 bytes of codes, each
+//    writing its four 16-byte results in a rotated order so that a store's eight lanes
+//    meet eight different bank groups.
+//  * Warps 12 and 13 issue the MMAs with the whole warp in step and one lane's predicate on the
+//    instruction: an M = 64, N = 64 MMA then takes 32 cycles (its rate); issued from a branch of
+//    one thread it took 55.
+//  * Warps 0-3 run the online softmax (fp32, exp2).  Weights are kept 2^6 above 1, so that
+//    fp16 reaches down to 2^-31 of the largest; O is rescaled when a head's maximum grows by more
+//    than 2^8.
+//  * P lies in the chunk's RoPE column block, which is dead once Q.K^T has read it.
+constexpr int kH = 64, kD = 576, kDv = 512, kChunk = 64;
+constexpr int kBlk = kChunk * 128;            // one SW128 column block of a chunk: 64 rows x 128 B
+constexpr int kStageBytes = 9 * kBlk;         // 72 KB
+constexpr int kQBytes = 9 * (kH * 128);       // 72 KB
+constexpr int kTcThreads = 448, kTcWarps = 14;
+constexpr int kWarpQK = 12, kWarpPV = 13;
+constexpr int kProdWarps = 8;
+constexpr int kHalfBlocks = 4;                // column blocks of a stage's first half
+constexpr size_t kTcSmem = 1024 + kQBytes + 2 * kStageBytes;
+constexpr int kMaxSplits = 64;
+constexpr int kMaxCluster = 8;
+constexpr int kOPitchF32 = kDv * 4 + 16;      // staged O rows (padded)
+constexpr int kOPitchBF16 = kDv * 2 + 16;
+static_assert(kH * kOPitchF32 + 4 * (2 * kH + kH / 2 * (kMaxCluster + 2)) <= 2 * kStageBytes,
+              "staged O, (m, l) and the merge weights fit in the stages");
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescale = 8.0f;              // log2 of the tolerated growth before O is rescaled
+constexpr float kLift = 6.0f;                 // log2 of the largest weight when the maximum is current
+
+struct TcBars {
+    uint64_t kfull[2][2], kempty[2][2];       // [stage][half]
+    uint64_t sfull[2], sempty[2];
+    uint64_t pfull[2];
+    uint64_t ofull[2];                        // P.V of chunk c done (per chunk parity)
+    uint64_t odone;                           // every P.V of this CTA done
+    uint64_t qconv;                           // Q's content is fp16 now
+    uint32_t tmem_base;
+    int nsel;
+    float qscale[kH];                         // 2^-e of head h: the true q is the stored one times it
+};
+
+// kind::f16 MMA issued by the lane(s) whose `on` is set, the whole warp in step.
+__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
+    if (on) mma_commit(bar);
+    __syncwarp();
+}
+// The same instruction descriptor with fp16 operands.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t bf16) { return bf16 & ~((1u << 7) | (1u << 10)); }
+
+// A bounded wait that the whole warp leaves with one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int where) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, where));
+}
+
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Two floats -> two fp16 packed (low half = a).
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+// Eight E2M1 codes (low nibble first) times the scale (in both halves) -> eight fp16, exact.
+__device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t s2) {
+    uint32_t a, b, c, d;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+        : "r"(w));
+    return make_uint4(f16x2_mul(a, s2), f16x2_mul(b, s2), f16x2_mul(c, s2), f16x2_mul(d, s2));
+}
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t code) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(code * 0x0101u));
+    return r;
+}
+
+// A lane's part of its warp's eight rows of a chunk: rows lane/8 and 4 + lane/8; of each, in either
+// half of the columns, codes 16 (lane & 7) .. + 15 (as bytes), their scale, and RoPE bytes
+// 16 (lane & 7) .. + 15.
+struct RawRows {
+    uint4 codes[2][2], rope[2];   // [half][row], [row]
+    uint32_t scale[2][2];
+};
+
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attend_kv4_tc_kernel(const AttendKv4Args a, int tiles, int splits, int cmerge, float* __restrict__ part_o,
+                         float* __restrict__ part_ml, int* status) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ TcBars bars;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* q_s = smem;
+    uint8_t* stage_s = smem + kQBytes;
+    float* ml_s = reinterpret_cast<float*>(stage_s + kH * kOPitchF32);   // (m, l) beside the staged O
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t unit = blockIdx.x / splits;            // (query, head tile)
+    const int sp = blockIdx.x - (int)(unit * splits);
+    const int64_t g = unit / tiles;
+    const int h0 = (int)(unit - g * tiles) * kH;
+    const int nh = min(kH, a.H - h0);
+    const int64_t b = g / a.Q;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            for (int hf = 0; hf < 2; ++hf) {
+                mbar_init(&bars.kfull[i][hf], kProdWarps);
+                mbar_init(&bars.kempty[i][hf], 1);
+            }
+            mbar_init(&bars.pfull[i], 128);
+            mbar_init(&bars.sfull[i], 1);
+            mbar_init(&bars.sempty[i], 128);
+            mbar_init(&bars.ofull[i], 1);
+        }
+        mbar_init(&bars.odone, 1);
+        mbar_init(&bars.qconv, 128);
+        fence_barrier_init();
+        bars.nsel = a.k;
+    }
+    if (warp == kWarpQK) {
+        tmem_alloc(&bars.tmem_base, 512);
+        tmem_relinquish();
+    }
+    const Kv4Window wp = kv4_window(a, g, b);
+    const int64_t n = kv4_entries(a, b, status);
+    const int nwc = (int)((wp.n + kChunk - 1) / kChunk);
+    const int32_t* sel = a.idx != nullptr ? a.idx + g * a.k : nullptr;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base;
+
+    // ---- selection length (CSA: the valid prefix of idx)
+    int nsel;
+    if (sel != nullptr) {
+        int first_bad = a.k;
+        for (int i = threadIdx.x; i < a.k; i += kTcThreads) {
+            const int32_t v = __ldg(sel + i);
+            if (v < 0 || v >= n) first_bad = min(first_bad, i);
+            if (v >= n) set_status(status, LCS_ERR_DEVICE, 603);
+        }
+        first_bad = __reduce_min_sync(0xffffffffu, first_bad);
+        if (lane == 0 && first_bad < a.k) atomicMin(&bars.nsel, first_bad);
+        __syncthreads();
+        nsel = bars.nsel;
+    } else {
+        nsel = (int)kv4_avail(a, g, n);
+    }
+    const int nch_all = nwc + (nsel + kChunk - 1) / kChunk;
+    const int nch = sp < nch_all ? (nch_all - sp + splits - 1) / splits : 0;      // this split's chunks
+    const int nwl = sp < nwc ? (nwc - sp + splits - 1) / splits : 0;              // window chunks among them, first
+    auto gcof = [&](int c) -> int { return sp + splits * c; };
+    auto chunk_valid = [&](int gc) -> int {
+        const int64_t v = gc < nwc ? wp.n - (int64_t)gc * kChunk : (int64_t)nsel - (int64_t)(gc - nwc) * kChunk;
+        return (int)(v < kChunk ? v : kChunk);
+    };
+
+    // ---- producers' first rows are on their way while every warp brings in Q
+    const bool producer = warp >= 4 && warp < 12;
+    const int pw = warp - 4;
+    const int r0 = pw * 8 + (lane >> 3);   // this lane's rows of a chunk: r0, r0 + 4
+    auto row_of = [&](int gc, int r) -> const uint8_t* {   // entry row r of compressed chunk gc, or null
+        const int j = (gc - nwc) * kChunk + r;
+        if (j >= nsel) return nullptr;
+        return kv4_row(a, b, sel != nullptr ? __ldg(sel + j) : j, status);
+    };
+    auto load_rows = [&](RawRows& x, const uint8_t* const (&src)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint8_t* p = src[i] + 16 * (lane & 7);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                x.codes[hf][i] = make_uint4(0, 0, 0, 0);
+                x.scale[hf][i] = 0;
+                if (src[i] != nullptr) {
+                    x.codes[hf][i] = __ldg(reinterpret_cast<const uint4*>(p + 128 * hf));
+                    x.scale[hf][i] = __ldg(src[i] + 384 + 8 * hf + (lane & 7));
+                }
+            }
+            x.rope[i] = make_uint4(0, 0, 0, 0);
+            if (src[i] != nullptr) x.rope[i] = __ldg(reinterpret_cast<const uint4*>(p + 256));
+        }
+    };
+    RawRows raw;
+    const uint8_t* nxt[2] = {nullptr, nullptr};
+    if (producer && nwl < nch) {
+        const uint8_t* src[2] = {row_of(gcof(nwl), r0), row_of(gcof(nwl), r0 + 4)};
+        load_rows(raw, src);
+        if (nwl + 1 < nch) {
+            nxt[0] = row_of(gcof(nwl + 1), r0);
+            nxt[1] = row_of(gcof(nwl + 1), r0 + 4);
+        }
+    }
+    // ---- Q: warp w takes heads w, w + 14, ...; scaled by 2^e, content to fp16 unless window chunks
+    // come first, in the SW128 layout (column block c/8, 16-byte chunk c%8 of row h)
+    if (nch > 0) {
+        constexpr int kHeads = (kH + kTcWarps - 1) / kTcWarps;
+        uint4 v[kHeads][3];
+        const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (g * a.H + h0) * kD);
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {
+                const int h = warp + kTcWarps * i;
+                v[i][c] = make_uint4(0, 0, 0, 0);
+                if (h < nh && (c < 2 || lane < 8)) v[i][c] = __ldg(qg + h * (kD / 8) + c * 32 + lane);
+            }
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            const int h = warp + kTcWarps * i;
+            if (h >= kH) continue;
+            uint32_t mag = 0;   // largest magnitude, as bf16 bits
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {
+                const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mag = max(mag, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+            }
+            mag = __reduce_max_sync(0xffffffffu, mag);
+            const int ex = (int)(mag >> 7) - 127;             // of the largest element (subnormals: -127)
+            int e = mag == 0 || mag >= 0x7F80u ? 0 : 14 - ex;   // zero, infinite or NaN heads stay as they are
+            e = e > 126 ? 126 : e;
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            if (lane == 0) bars.qscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {
+                if (c == 2 && lane >= 8) continue;
+                const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float f0 = __uint_as_float(w[k] << 16) * up, f1 = __uint_as_float(w[k] & 0xFFFF0000u) * up;
+                    o[k] = c < 2 && nwl == 0 ? pack_f16x2(f0, f1) : pack_bf16x2(f0, f1);
+                }
+                const int ch = c * 32 + lane;
+                *reinterpret_cast<uint4*>(q_s + (ch >> 3) * (kH * 128) + sw128_off(h, ch & 7)) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+
+    constexpr uint32_t id_qk_b = idesc_bf16(64, kChunk, false, false), id_qk_h = idesc_f16(id_qk_b);
+    constexpr uint32_t id_pv_b = idesc_bf16(64, 256, false, true), id_pv_h = idesc_f16(id_pv_b);
+    auto t_s = [&](int buf) { return tmem + 256u + 64u * (uint32_t)buf; };
+    const uint32_t on = lane == 0 ? 1u : 0u;   // the issuing lane
+
+    if (warp == kWarpQK) {
+        // ---------------- Q.K^T issue
+        const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024);
+        const uint64_t k_desc0 = sw128_desc(smem_u32(stage_s), 16, 1024);
+        bool ok = true;
+        for (int c = 0; c < nch && ok; ++c) {
+            const int st = c & 1;
+            if (nwl > 0 && c == nwl && !warp_wait(&bars.qconv, 0, status, 604)) break;
+            if (c >= 2 && !warp_wait(&bars.sempty[st], (uint32_t)(((c - 2) >> 1) & 1), status, 605)) break;
+            const uint64_t kd = k_desc0 + (uint64_t)((st * kStageBytes) >> 4);
+            const uint32_t id = c < nwl ? id_qk_b : id_qk_h;
+            if (!warp_wait(&bars.kfull[st][0], (uint32_t)((c >> 1) & 1), status, 606)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < 4 * kHalfBlocks; ++s)
+                mma_ss_if(on, t_s(st), q_desc + (uint64_t)(((s >> 2) * (kH * 128) + (s & 3) * 32) >> 4),
+                          kd + (uint64_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), id, s ? 1u : 0u);
+            if (!warp_wait(&bars.kfull[st][1], (uint32_t)((c >> 1) & 1), status, 607)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int s = 4 * kHalfBlocks; s < 36; ++s)
+                mma_ss_if(on, t_s(st), q_desc + (uint64_t)(((s >> 2) * (kH * 128) + (s & 3) * 32) >> 4),
+                          kd + (uint64_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), s < 32 ? id : id_qk_b, 1u);
+            commit_if(on, &bars.sfull[st]);
+        }
+    } else if (warp == kWarpPV) {
+        // ---------------- P.V issue (its own warp: it never waits behind the next Q.K^T's rows)
+        const uint64_t k_desc0 = sw128_desc(smem_u32(stage_s), 16, 1024);
+        const uint64_t v_desc0 = sw128_desc(smem_u32(stage_s), kBlk, 1024);
+        for (int c = 0; c < nch; ++c) {
+            const int st = c & 1;
+            if (!warp_wait(&bars.pfull[st], (uint32_t)((c >> 1) & 1), status, 608)) break;
+            tc_fence_after();
+            const uint64_t pd = k_desc0 + (uint64_t)((st * kStageBytes + 8 * kBlk) >> 4);
+            const uint64_t vd = v_desc0 + (uint64_t)((st * kStageBytes) >> 4);
+            const uint32_t id = c < nwl ? id_pv_b : id_pv_h;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ss_if(on, tmem + (half ? (16u << 16) : 0u), pd + (uint64_t)((kk * 32) >> 4),
+                              vd + (uint64_t)((half * kHalfBlocks * kBlk + kk * 2048) >> 4), id, (c | kk) ? 1u : 0u);
+                // dims 0-255 read column blocks 0-3; blocks 4-8 are released after the rest
+                commit_if(on, &bars.kempty[st][half]);
+            }
+            commit_if(on, &bars.ofull[st]);
+        }
+        if (nch > 0) commit_if(on, &bars.odone);
+    } else if (producer) {
+        // ---------------- producers: this split's chunks in order, stage c & 1
+        for (int c = 0; c < nch; ++c) {
+            const int st = c & 1;
+            uint8_t* dst = stage_s + st * kStageBytes;
+            const uint32_t par = (uint32_t)((((c >> 1) - 1)) & 1);
+            if (c < nwl) {
+                // window chunk: bf16 rows by 16-byte cp.async, zeros past the last row
+                if (c >= 2 && (!warp_wait(&bars.kempty[st][0], par, status, 609) ||
+                               !warp_wait(&bars.kempty[st][1], par, status, 610)))
+                    break;
+                const int gc = gcof(c), nv = chunk_valid(gc);
+                const uint8_t* w0 = static_cast<const uint8_t*>(a.win) +
+                                    (b * a.Tw + wp.lo + (int64_t)gc * kChunk) * (kD * 2);
+                for (int i = 0; i < 8; ++i) {
+                    const int r = pw * 8 + i;
+                    const bool valid = r < nv;
+                    for (int ch = lane; ch < 72; ch += 32)
+                        cp_async_16(dst + (ch >> 3) * kBlk + sw128_off(r, ch & 7), w0 + (valid ? r * (kD * 2) + ch * 16 : 0),
+                                    valid);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars.kfull[st][0]);
+                    mbar_arrive(&bars.kfull[st][1]);
+                }
+                continue;
+            }
+            bool ok = true;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                if (c >= 2 && !warp_wait(&bars.kempty[st][hf], par, status, 611 + hf)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = r0 + 4 * i;
+                    const uint32_t s2 = scale_f16x2(raw.scale[hf][i]);
+                    const uint4 cv = raw.codes[hf][i];
+                    // codes 32 p .. 32 p + 31 of the row, p = 8 hf + (lane & 7): chunks 4 (p & 1) + 0..3 of block p / 2
+                    uint8_t* blk = dst + (4 * hf + ((lane & 7) >> 1)) * kBlk;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int q = (k + ((lane & 7) >> 1)) & 3;
+                        const uint32_t w = q & 2 ? (q & 1 ? cv.w : cv.z) : (q & 1 ? cv.y : cv.x);
+                        *reinterpret_cast<uint4*>(blk + sw128_off(r, 4 * (lane & 1) + q)) = widen8(w, s2);
+                    }
+                    if (hf) *reinterpret_cast<uint4*>(dst + 8 * kBlk + sw128_off(r, lane & 7)) = raw.rope[i];
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.kfull[st][hf]);
+            }
+            if (!ok) break;
+            // the next chunk's rows into the registers, and where the one after lies
+            if (c + 1 < nch) {
+                load_rows(raw, nxt);
+                if (c + 2 < nch) {
+                    nxt[0] = row_of(gcof(c + 2), r0);
+                    nxt[1] = row_of(gcof(c + 2), r0 + 4);
+                }
+            }
+        }
+    } else if (warp < 4) {
+        // ---------------- softmax: warp q owns heads 16q..16q+15; lane l works on head 16q + (l & 15), on
+        // S columns 0-31 (lanes 0-15) or 32-63 (lanes 16-31)
+        const int head = warp * 16 + (lane & 15);
+        const int cbase = (lane < 16) ? 0 : 32;
+        float m_used = -INFINITY, l_sum = 0.f;   // log2 domain; weights are 2^(s - m_used + kLift)
+        const float sl2 = nch > 0 ? a.scale * kLog2e * bars.qscale[head] : 0.f;
+        for (int c = 0; c < nch; ++c) {
+            const int st = c & 1;
+            const bool wchunk = c < nwl;
+            if (!warp_wait(&bars.sfull[st], (uint32_t)((c >> 1) & 1), status, 620)) break;
+            tc_fence_after();
+            if (wchunk && c + 1 == nwl && nwl < nch) {
+                // the last window chunk's Q.K^T is done: Q's content to fp16, in place
+                for (int i = threadIdx.x; i < kH * 64; i += 128) {
+                    uint4* p = reinterpret_cast<uint4*>(q_s) + i;
+                    const uint4 v = *p;
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        o[k] = pack_f16x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+                    *p = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars.qconv);
+            }
+            uint32_t sv[32];
+            tmem_ld16x2_32(tmem_addr(t_s(st), warp * 32, 0), sv);
+            tmem_ld_wait();
+            tc_fence_before();
+            mbar_arrive(&bars.sempty[st]);
+            const int nv = chunk_valid(gcof(c)) - cbase;   // this lane's valid columns
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < nv) mx = fmaxf(mx, __uint_as_float(sv[j]) * sl2);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            float alpha = 1.f;
+            bool rescale = false;
+            if (mx > m_used + kRescale || m_used == -INFINITY) {
+                const float m_new = fmaxf(mx, m_used);
+                alpha = (m_used == -INFINITY) ? 0.f : exp2f(m_used - m_new);
+                rescale = (c > 0);
+                m_used = m_new;
+            }
+            const float off = m_used == -INFINITY ? 0.f : m_used - kLift;   // every score -inf: weights 0
+            uint8_t* pblk = stage_s + st * kStageBytes + 8 * kBlk;
+            float psum = 0.f;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int j = ch * 8 + 2 * q;
+                    const float p0 = j < nv ? exp2f(__uint_as_float(sv[j]) * sl2 - off) : 0.f;
+                    const float p1 = j + 1 < nv ? exp2f(__uint_as_float(sv[j + 1]) * sl2 - off) : 0.f;
+                    pk[q] = wchunk ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+                    psum += p0 + p1;
+                }
+                *reinterpret_cast<uint4*>(pblk + sw128_off(head, (cbase >> 3) + ch)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+            psum += __shfl_xor_sync(0xffffffffu, psum, 16);
+            l_sum = l_sum * alpha + psum;
+            if (__any_sync(0xffffffffu, rescale)) {
+                // O may be written once the previous chunk's P.V is done
+                if (!warp_wait(&bars.ofull[(c - 1) & 1], (uint32_t)(((c - 1) >> 1) & 1), status, 621)) break;
+                tc_fence_after();
+                const float f = rescale ? alpha : 1.f;
+                for (int j = 0; j < 256 / 16; ++j) {
+                    uint32_t ov[16];
+                    const uint32_t ta = tmem_addr(tmem, warp * 32, j * 16);
+                    tmem_ld16(ta, ov);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * f);
+                    tmem_st16(ta, ov);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bars.pfull[st]);
+        }
+        // ---- O (normalised when this is the only split; else the partial O and (m, l)) staged through
+        // shared memory.  Lane l of warp q holds the O row of head 16q + (l & 15), dims 0-255 (lanes
+        // 0-15) or 256-511 (lanes 16-31).
+        if (nch > 0) warp_wait(&bars.odone, 0, status, 622);
+        tc_fence_after();
+        const bool final_out = splits == 1;
+        const float fs = final_out ? ((l_sum > 0.f) ? 1.f / l_sum : 0.f) : 1.f;
+        const int dim0 = (lane < 16) ? 0 : 256;
+        const bool f32 = !final_out || a.out_dtype == LCS_F32;
+        uint8_t* rowp = stage_s + head * (f32 ? kOPitchF32 : kOPitchBF16);
+        for (int j0 = 0; j0 < 256 / 16; j0 += 4) {
+            uint32_t ov[4][16];
+            if (nch > 0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) tmem_ld16(tmem_addr(tmem, warp * 32, (j0 + u) * 16), ov[u]);
+                tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) ov[u][q] = 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = j0 + u;
+                if (f32) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        reinterpret_cast<float4*>(rowp + (dim0 + j * 16) * 4)[q] =
+                            make_float4(__uint_as_float(ov[u][4 * q]) * fs, __uint_as_float(ov[u][4 * q + 1]) * fs,
+                                        __uint_as_float(ov[u][4 * q + 2]) * fs, __uint_as_float(ov[u][4 * q + 3]) * fs);
+                } else {
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        pk[q] = pack_bf16x2(__uint_as_float(ov[u][2 * q]) * fs, __uint_as_float(ov[u][2 * q + 1]) * fs);
+                    reinterpret_cast<uint4*>(rowp + (dim0 + j * 16) * 2)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    reinterpret_cast<uint4*>(rowp + (dim0 + j * 16) * 2)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                }
+            }
+        }
+        if (lane < 16) {
+            const float m = l_sum > 0.f ? m_used - kLift : -INFINITY;
+            if (final_out) {
+                if (a.lse != nullptr && head < nh)
+                    a.lse[g * a.H + h0 + head] = l_sum > 0.f ? (m + log2f(l_sum)) / kLog2e : -INFINITY;
+            } else {
+                float* ml = cmerge ? ml_s + 2 * head : part_ml + ((unit * splits + sp) * kH + head) * 2;
+                ml[0] = m;
+                ml[1] = l_sum;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (cmerge) {
+        // ---- split merge inside the cluster: split sp merges heads sp, sp + splits, ... from every
+        // split's staged O and (m, l) over distributed shared memory, in split order
+        cluster_sync_all();
+        constexpr int kW = kMaxCluster + 2;
+        float* wt = ml_s + 2 * kH;   // [heads of this split][f_0 .. f_{splits-1}, 1/L]
+        const int nm = sp < nh ? (nh - sp + splits - 1) / splits : 0;
+        if ((int)threadIdx.x < nm) {
+            const int h = sp + (int)threadIdx.x * splits;
+            float M = -INFINITY;
+            for (int r = 0; r < splits; ++r) {
+                const float m = ld_dsmem_f32(dsmem_addr(ml_s + 2 * h, (uint32_t)r));
+                const float l = ld_dsmem_f32(dsmem_addr(ml_s + 2 * h + 1, (uint32_t)r));
+                if (l > 0.f) M = fmaxf(M, m);
+            }
+            float Ls = 0.f;
+            for (int r = 0; r < splits; ++r) {
+                const float m = ld_dsmem_f32(dsmem_addr(ml_s + 2 * h, (uint32_t)r));
+                const float l = ld_dsmem_f32(dsmem_addr(ml_s + 2 * h + 1, (uint32_t)r));
+                const float f = l > 0.f ? exp2f(m - M) : 0.f;
+                wt[threadIdx.x * kW + r] = f;
+                Ls += l * f;
+            }
+            wt[threadIdx.x * kW + kMaxCluster] = Ls > 0.f ? 1.f / Ls : 0.f;
+            if (a.lse != nullptr) a.lse[g * a.H + h0 + h] = Ls > 0.f ? (M + log2f(Ls)) / kLog2e : -INFINITY;
+        }
+        __syncthreads();
+        for (int it = (int)threadIdx.x; it < nm * (kDv / 4); it += kTcThreads) {
+            const int i = it / (kDv / 4), q4 = it - i * (kDv / 4);
+            const int h = sp + i * splits;
+            const float* rw = wt + i * kW;
+            const uint8_t* src = stage_s + h * kOPitchF32 + q4 * 16;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < splits; ++r) {
+                const float4 v = ld_dsmem_f4(dsmem_addr(src, (uint32_t)r));
+                const float f = rw[r];
+                acc.x += v.x * f;
+                acc.y += v.y * f;
+                acc.z += v.z * f;
+                acc.w += v.w * f;
+            }
+            const float iv = rw[kMaxCluster];
+            const int64_t o4 = (g * a.H + h0 + h) * (kDv / 4) + q4;
+            if (a.out_dtype == LCS_F32)
+                reinterpret_cast<float4*>(a.out)[o4] = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
+            else
+                reinterpret_cast<uint2*>(a.out)[o4] =
+                    make_uint2(pack_bf16x2(acc.x * iv, acc.y * iv), pack_bf16x2(acc.z * iv, acc.w * iv));
+        }
+        cluster_sync_all();   // no CTA leaves while a peer still reads its staged partial
+    } else {
+        // the staged rows (the output's heads, or this split's partial) with coalesced 16-byte stores
+        const bool f32 = splits > 1 || a.out_dtype == LCS_F32;
+        const int pitch = f32 ? kOPitchF32 : kOPitchBF16;
+        const int rb = f32 ? kDv * 4 : kDv * 2;
+        uint8_t* gout = splits == 1 ? static_cast<uint8_t*>(a.out) + (g * a.H + h0) * rb
+                                    : reinterpret_cast<uint8_t*>(part_o + (unit * splits + sp) * kH * kDv);
+        const int rows = splits == 1 ? nh : kH;
+        for (int off = (int)threadIdx.x * 16; off < rows * rb; off += kTcThreads * 16) {
+            const int h = off / rb, cb = off - h * rb;
+            *reinterpret_cast<uint4*>(gout + off) = *reinterpret_cast<const uint4*>(stage_s + h * pitch + cb);
+        }
+    }
+#if defined(__CUDA_ARCH__)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the split combine
+#endif
+    if (warp == kWarpQK) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Merges the split partials of one (query, head) per CTA: 128 threads, one float4 of the 512 output
+// dims each; weights 2^(m_s - M) and 1/L formed once; sums in split order, eight loads at a time.
+__global__ void __launch_bounds__(128) kv4_combine_kernel(const float* __restrict__ part_o,
+                                                          const float* __restrict__ part_ml, int splits, int H, int tiles,
+                                                          void* __restrict__ out, int out_dtype, float* __restrict__ lse) {
+    __shared__ float fac[kMaxSplits];
+    __shared__ float inv_l;
+    const int64_t gh = blockIdx.x;   // query * H + head
+    const int64_t g = gh / H;
+    const int hh = (int)(gh - g * H), t = threadIdx.x;
+    const int64_t unit = g * tiles + hh / kH;
+    const int h = hh % kH;
+#if defined(__CUDA_ARCH__)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+#endif
+    if (t < 32) {
+        float2 ml[2];
+        float M = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int s = t + 32 * i;
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (s < splits) ml[i] = __ldcg(reinterpret_cast<const float2*>(part_ml) + (unit * splits + s) * kH + h);
+            M = fmaxf(M, ml[i].x);
+        }
+        M = warp_max(M);
+        float L = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float e = ml[i].y > 0.f ? exp2f(ml[i].x - M) : 0.f;
+            if (t + 32 * i < splits) fac[t + 32 * i] = e;
+            L += ml[i].y * e;
+        }
+        L = warp_sum(L);   // a fixed tree
+        if (t == 0) {
+            inv_l = L > 0.f ? 1.f / L : 0.f;
+            if (lse != nullptr) lse[gh] = L > 0.f ? (M + log2f(L)) / kLog2e : -INFINITY;
+        }
+    }
+    __syncthreads();
+    const float4* src = reinterpret_cast<const float4*>(part_o) + (unit * splits * kH + h) * (kDv / 4) + t;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < splits; s0 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (s0 + i < splits) v[i] = __ldcg(src + (int64_t)(s0 + i) * kH * (kDv / 4));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (s0 + i < splits) {
+                const float e = fac[s0 + i];
+                acc.x += v[i].x * e;
+                acc.y += v[i].y * e;
+                acc.z += v[i].z * e;
+                acc.w += v[i].w * e;
+            }
+    }
+    const float iv = inv_l;
+    if (out_dtype == LCS_F32)
+        reinterpret_cast<float4*>(out)[gh * (kDv / 4) + t] = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
+    else
+        reinterpret_cast<uint2*>(out)[gh * (kDv / 4) + t] =
+            make_uint2(pack_bf16x2(acc.x * iv, acc.y * iv), pack_bf16x2(acc.z * iv, acc.w * iv));
+}
+
+bool use_tc(const AttendKv4Args& a) { return a.q_dtype == LCS_BF16 && a.d_c == kDv && a.d_r == kD - kDv; }
+
+// Splits per (query, head tile): every CTA resident at once (one per SM), at least two chunks a
+// split; the count that minimises the longest split's chunks plus a fixed cost of about two chunks
+// (prologue, fill, epilogue) and, with splits, of the merge, which grows with their number.
+int kv4_splits(const AttendKv4Args& a) {
+    const int64_t units = a.B * a.Q * ((a.H + kH - 1) / kH);
+    const int64_t most_w = a.q_pos == nullptr ? a.Tw : (a.W < a.Tw ? a.W : a.Tw);
+    const int64_t chunks = (most_w + kChunk - 1) / kChunk +
+                           ((a.idx != nullptr ? a.k : a.max_blocks * a.be) + kChunk - 1) / kChunk;
+    int best = 1;
+    double best_cost = (double)chunks + 2.0;
+    for (int s = 2; s <= kMaxSplits; ++s) {
+        if ((chunks + s - 1) / s < 2 || units * s > num_sms()) break;
+        const double cost = (double)((chunks + s - 1) / s) + 3.0 + s / 16.0;
+        if (cost < best_cost) {
+            best = s;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+// Whether all of the launch's clusters of `splits` CTAs can be resident at once (asked once per
+// device and split count).
+bool kv4_cluster_ok(int splits, int64_t units) {
+    if (splits < 2 || splits > kMaxCluster) return false;
+    constexpr int kDevices = 16;
+    static std::mutex mu;
+    static int cache[kDevices][kMaxCluster + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (cache[dev][splits] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)splits);
+        cfg.blockDim = dim3(kTcThreads);
+        cfg.dynamicSmemBytes = kTcSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)splits;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, attend_kv4_tc_kernel, &cfg) != cudaSuccess) n = 0;
+        cudaGetLastError();
+        cache[dev][splits] = n > 0 ? n : -1;
+    }
+    return cache[dev][splits] >= units;
+}
+
+cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaStream_t s) {
+    const int tiles = (a.H + kH - 1) / kH;
+    const int64_t units = a.B * a.Q * tiles;
+    cudaError_t e = set_smem_here(reinterpret_cast<const void*>(attend_kv4_tc_kernel), kTcSmem);
+    if (e != cudaSuccess) return e;
+    const int splits = kv4_splits(a);
+    float* part_o = nullptr;
+    float* part_ml = nullptr;
+    if (splits > 1) {
+        part_o = static_cast<float*>(scratch);
+        part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + align256(units * splits * kH * kDv * 4));
+    }
+    const int cmerge = kv4_cluster_ok(splits, units) ? 1 : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * splits));
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = kTcSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cmerge;
+    e = cudaLaunchKernelEx(&cfg, attend_kv4_tc_kernel, a, tiles, splits, cmerge, part_o, part_ml, status);
+    if (e != cudaSuccess || splits == 1 || cmerge) return e;
+    return launch_k(kv4_combine_kernel, dim3((unsigned)(a.B * a.Q * a.H)), dim3(128), 0, s, true, part_o, part_ml, splits,
+                    a.H, tiles, a.out, a.out_dtype, a.lse);
+}
+
 }  // namespace
 
-int64_t attend_kv4_scratch_bytes(const AttendKv4Args&) { return 0; }
+// Split partials: fp32 O [units, splits, 64, 512] and (m, l) [units, splits, 64, 2].
+int64_t attend_kv4_scratch_bytes(const AttendKv4Args& a) {
+    if (!use_tc(a)) return 0;
+    const int s = kv4_splits(a);
+    if (s == 1) return 0;
+    const int64_t units = a.B * a.Q * ((a.H + kH - 1) / kH);
+    return align256(units * s * kH * kDv * 4) + align256(units * s * kH * 2 * 4);
+}
 
-cudaError_t launch_attend_kv4(const AttendKv4Args& a, void*, int* status, cudaStream_t s) {
+cudaError_t launch_attend_kv4(const AttendKv4Args& a, void* scratch, int* status, cudaStream_t s) {
     const int64_t queries = a.B * a.Q;
     if (queries == 0) return cudaSuccess;
+    if (use_tc(a)) return launch_tc(a, scratch, status, s);
     const int D = a.d_c + a.d_r;
     const size_t smem = sizeof(float) * (kSHeads * D + kSRows * (D + 1) + kSHeads * (kSRows + 1) + 2 * kSHeads);
     cudaError_t e = set_smem_here(reinterpret_cast<const void*>(attend_kv4_kernel), smem);
