@@ -56,14 +56,11 @@ __device__ __forceinline__ Kv4Window kv4_window(const AttendKv4Args& a, int64_t 
 }
 
 // Row of entry e (0 <= e < kv4_entries) of request b, or null when its block is not one of the
-// pool's (recorded in the status word).
-__device__ __forceinline__ const uint8_t* kv4_row(const AttendKv4Args& a, int64_t b, int e, int* status) {
+// pool's.
+__device__ __forceinline__ const uint8_t* kv4_row(const AttendKv4Args& a, int64_t b, int e) {
     const int bi = e / a.be;
     const int32_t id = __ldg(a.table + b * a.max_blocks + bi);
-    if (id < 0 || id >= a.n_blocks) {
-        set_status(status, LCS_ERR_DEVICE, 602);
-        return nullptr;
-    }
+    if (id < 0 || id >= a.n_blocks) return nullptr;
     return a.pool + ((int64_t)id * a.be + (e - bi * a.be)) * a.row_bytes;
 }
 
@@ -102,12 +99,11 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
     if (sel != nullptr)
         for (int i = t; i < a.k; i += kSThreads) {
             const int32_t v = sel[i];
-            if (v >= 0 && v < n) continue;
-            if (v >= n) set_status(status, LCS_ERR_DEVICE, 603);
-            atomicMin(&nsel_s, i);
+            if (v < 0 || v >= n) atomicMin(&nsel_s, i);
         }
     __syncthreads();
     const int64_t nsel = nsel_s;
+    if (sel != nullptr && t == 0 && nsel < a.k && sel[nsel] >= 0) set_status(status, LCS_ERR_DEVICE, 603);
     const Kv4Window win = kv4_window(a, g, b);
     const int64_t R = nsel + win.n;
 
@@ -121,7 +117,8 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
         const int nc = (int)(nsel - r0 < 0 ? 0 : (nsel - r0 < nr ? nsel - r0 : nr));   // compressed rows among them
         for (int i = t; i < nc * blocks; i += kSThreads) {
             const int r = i / blocks, bl = i - r * blocks;
-            const uint8_t* src = kv4_row(a, b, sel != nullptr ? sel[r0 + r] : (int)(r0 + r), status);
+            const uint8_t* src = kv4_row(a, b, sel != nullptr ? sel[r0 + r] : (int)(r0 + r));
+            if (src == nullptr) set_status(status, LCS_ERR_DEVICE, 602);
             float* o = rows + r * pitch + 32 * bl;
             const uint4 c = src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src) + bl) : make_uint4(0, 0, 0, 0);
             const float s = src != nullptr ? e4m3_to_f32(src[a.d_c / 2 + 2 * a.d_r + bl]) : 0.f;
@@ -135,7 +132,7 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
         }
         for (int i = t; i < nc * a.d_r; i += kSThreads) {
             const int r = i / a.d_r, j = i - r * a.d_r;
-            const uint8_t* src = kv4_row(a, b, sel != nullptr ? sel[r0 + r] : (int)(r0 + r), status);
+            const uint8_t* src = kv4_row(a, b, sel != nullptr ? sel[r0 + r] : (int)(r0 + r));
             rows[r * pitch + a.d_c + j] =
                 src != nullptr ? bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(src + a.d_c / 2 + 2 * j)) : 0.f;
         }
@@ -217,9 +214,9 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
 //    a lane) while it waits for its stage; eight lanes take one row's 128 bytes of codes, each
 //    writing its four 16-byte results in a rotated order so that a store's eight lanes
 //    meet eight different bank groups.
-//  * Warps 12 and 13 issue the MMAs with the whole warp in step and one lane's predicate on the
-//    instruction: an M = 64, N = 64 MMA then takes 32 cycles (its rate); issued from a branch of
-//    one thread it took 55.
+//  * Warps 12 and 13 issue the MMAs with the whole warp in step and an elected lane's predicate on
+//    the instruction: 35 cycles per M = 64, N = 64 MMA alone on the SM (32 is its rate), where
+//    issue from a branch of one thread took 55 to 72 and was what a chunk waited for.
 //  * Warps 0-3 run the online softmax (fp32, exp2).  Weights are kept 2^6 above 1, so that
 //    fp16 reaches down to 2^-31 of the largest; O is rescaled when a head's maximum grows by more
 //    than 2^8.
@@ -251,23 +248,38 @@ struct TcBars {
     uint64_t odone;                           // every P.V of this CTA done
     uint64_t qconv;                           // Q's content is fp16 now
     uint32_t tmem_base;
-    int nsel;
+    int first_bad[kTcWarps];
     float qscale[kH];                         // 2^-e of head h: the true q is the stored one times it
 };
 
-// kind::f16 MMA issued by the lane(s) whose `on` is set, the whole warp in step.
-__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// One lane of the (converged) warp, the same at every call.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+// kind::f16 MMA issued by the elected lane, the whole warp in step.  a, b: the low words of the
+// operands' descriptors (address and lbo), hi: their common high word (sbo, version, swizzle).
+__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                          uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.ne.b32 e, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
+        "mov.b64 da, {%1, %6};\n\t"
+        "mov.b64 db, {%2, %6};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(on), "r"(hi)
         : "memory");
 }
+// The elected lane's commit: arrives once on `bar` when its MMAs so far are complete.
 __device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
-    if (on) mma_commit(bar);
-    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(on)
+        : "memory");
 }
 // The same instruction descriptor with fp16 operands.
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t bf16) { return bf16 & ~((1u << 7) | (1u << 10)); }
@@ -282,14 +294,22 @@ __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 // Two floats -> two fp16 packed (low half = a).
 __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-// Eight E2M1 codes (low nibble first) times the scale (in both halves) -> eight fp16, exact.
-__device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t s2) {
+// Eight E2M1 codes (low nibble first) times the scale (in both halves) -> eight fp16, exact.  Two
+// forms, so that neither pipe carries all of it: with the conversion instruction (16 lanes a
+// clock per SM, shared with exp2), and with byte permutes: the high byte of a magnitude's fp16 is
+// looked up by its three low bits (the low byte is 0), the sign bits are moved to the bytes' tops.
+__device__ __forceinline__ uint4 widen8_cvt(uint32_t w, uint32_t s2) {
     uint32_t a, b, c, d;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -301,18 +321,27 @@ __device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t s2) {
         : "r"(w));
     return make_uint4(f16x2_mul(a, s2), f16x2_mul(b, s2), f16x2_mul(c, s2), f16x2_mul(d, s2));
 }
-__device__ __forceinline__ uint32_t scale_f16x2(uint32_t code) {
+__device__ __forceinline__ uint4 widen8_perm(uint32_t w, uint32_t s2) {
+    constexpr uint32_t lo = 0x3E3C3800u, hi = 0x46444240u;   // 0, 0.5, 1, 1.5 | 2, 3, 4, 6
+    const uint32_t m = w & 0x77777777u, ws = w << 4;
+    const uint32_t r0 = __byte_perm(lo, hi, m) | (__byte_perm(ws, w, 0x5140) & 0x80808080u);
+    const uint32_t r1 = __byte_perm(lo, hi, m >> 16) | (__byte_perm(ws, w, 0x7362) & 0x80808080u);
+    return make_uint4(f16x2_mul(__byte_perm(r0, 0, 0x1404), s2), f16x2_mul(__byte_perm(r0, 0, 0x3424), s2),
+                      f16x2_mul(__byte_perm(r1, 0, 0x1404), s2), f16x2_mul(__byte_perm(r1, 0, 0x3424), s2));
+}
+// The E4M3 scale in byte `at` of w, as fp16 in both halves.
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t w, int at) {
     uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(code * 0x0101u));
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
+        : "=r"(r)
+        : "r"(__byte_perm(w, 0, (uint32_t)at * 0x11u)));
     return r;
 }
 
-// A lane's part of its warp's eight rows of a chunk: rows lane/8 and 4 + lane/8; of each, in either
-// half of the columns, codes 16 (lane & 7) .. + 15 (as bytes), their scale, and RoPE bytes
-// 16 (lane & 7) .. + 15.
-struct RawRows {
-    uint4 codes[2][2], rope[2];   // [half][row], [row]
-    uint32_t scale[2][2];
+// A lane's part of row lane & 7 of its warp's eight rows of a chunk: the 16-byte pieces p = (lane >> 3)
+// + 4 i of the codes (i < 4) and of the RoPE dims (i < 2), and the row's scales.
+struct RawRow {
+    uint4 codes[4], rope[2], scales;
 };
 
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -325,13 +354,80 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint8_t* stage_s = smem + kQBytes;
     float* ml_s = reinterpret_cast<float*>(stage_s + kH * kOPitchF32);   // (m, l) beside the staged O
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t unit = blockIdx.x / splits;            // (query, head tile)
-    const int sp = blockIdx.x - (int)(unit * splits);
-    const int64_t g = unit / tiles;
-    const int h0 = (int)(unit - g * tiles) * kH;
+    // values that steer whole warps come from lane 0, so that the compiler keeps them (and what the MMA
+    // issue derives from them) in uniform registers
+    auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const int warp = uni(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int unit = splits > 1 ? blockIdx.y : blockIdx.x;   // (query, head tile)
+    const int sp = splits > 1 ? blockIdx.x : 0;
+    const int g = tiles == 2 ? unit >> 1 : unit;
+    const int h0 = tiles == 2 ? (unit & 1) * kH : 0;
     const int nh = min(kH, a.H - h0);
-    const int64_t b = g / a.Q;
+    const int b = a.Q == 1 ? g : (int)((unsigned)g / (unsigned)a.Q);
+    const bool producer = warp >= 4 && warp < 12;
+    const int pw = warp - 4;
+
+    // ---- the loads that nothing waits for, before everything else: Q (warp w takes heads w, w + 14, ...) ...
+    constexpr int kHeads = (kH + kTcWarps - 1) / kTcWarps;
+    uint4 qv[kHeads][3];
+    {
+        const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + ((int64_t)g * a.H + h0) * kD);
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {
+                const int h = warp + kTcWarps * i;
+                qv[i][c] = make_uint4(0, 0, 0, 0);
+                if (h < nh && (c < 2 || lane < 8)) qv[i][c] = __ldg(qg + h * (kD / 8) + c * 32 + lane);
+            }
+    }
+    // ... and the producers' first rows.  Which of a chunk's rows are attended is known later (the
+    // selection's length): rows behind it are dropped when they are widened.
+    const Kv4Window wp = kv4_window(a, g, b);
+    const int64_t n = kv4_entries(a, b, status);
+    const int nwc = (int)((wp.n + kChunk - 1) / kChunk);
+    const int nwl = uni(sp < nwc ? (nwc - sp + splits - 1) / splits : 0);   // this split's window chunks, first
+    const int32_t* sel = a.idx != nullptr ? a.idx + (int64_t)g * a.k : nullptr;
+    const int most = sel != nullptr ? a.k : (int)kv4_avail(a, g, n);
+    auto gcof = [&](int c) -> int { return sp + splits * c; };
+    const int my_row = pw * 8 + (lane & 7);
+    auto row_of = [&](int c) -> const uint8_t* {   // this lane's row of local chunk c, null if there is none
+        const int j = (gcof(c) - nwc) * kChunk + my_row;
+        if (j >= most) return nullptr;
+        const int e = sel != nullptr ? __ldg(sel + j) : j;
+        return e >= 0 && e < n ? kv4_row(a, b, e) : nullptr;
+    };
+    RawRow raw;
+    auto load_row = [&](const uint8_t* src) {
+        const uint4* p = reinterpret_cast<const uint4*>(src) + (lane >> 3);
+        if (src != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw.codes[i] = __ldg(p + 4 * i);
+            raw.rope[0] = __ldg(p + 16);
+            raw.rope[1] = __ldg(p + 20);
+            raw.scales = __ldg(reinterpret_cast<const uint4*>(src) + 24);
+        }
+    };
+    // window chunk c of this split into stage c & 1: bf16 rows by 16-byte cp.async, zeros past the last row
+    auto load_window = [&](int c) {
+        uint8_t* dst = stage_s + (c & 1) * kStageBytes;
+        const int64_t w0 = (int64_t)gcof(c) * kChunk;
+        const uint8_t* src = static_cast<const uint8_t*>(a.win) + ((int64_t)b * a.Tw + wp.lo + w0) * (kD * 2);
+        for (int i = 0; i < 8; ++i) {
+            const int r = pw * 8 + i;
+            const bool valid = w0 + r < wp.n;
+            for (int ch = lane; ch < 72; ch += 32)
+                cp_async_16(dst + (ch >> 3) * kBlk + sw128_off(r, ch & 7), src + (valid ? r * (kD * 2) + ch * 16 : 0), valid);
+        }
+        cp_async_commit();
+    };
+    const uint8_t *cur = nullptr, *nxt = nullptr;
+    if (producer) {
+        cur = row_of(nwl);
+        load_row(cur);
+        if (nwl > 0) load_window(0);
+        nxt = row_of(nwl + 1);
+    }
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -347,179 +443,122 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(&bars.odone, 1);
         mbar_init(&bars.qconv, 128);
         fence_barrier_init();
-        bars.nsel = a.k;
     }
     if (warp == kWarpQK) {
         tmem_alloc(&bars.tmem_base, 512);
         tmem_relinquish();
     }
-    const Kv4Window wp = kv4_window(a, g, b);
-    const int64_t n = kv4_entries(a, b, status);
-    const int nwc = (int)((wp.n + kChunk - 1) / kChunk);
-    const int32_t* sel = a.idx != nullptr ? a.idx + g * a.k : nullptr;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = bars.tmem_base;
-
-    // ---- selection length (CSA: the valid prefix of idx)
-    int nsel;
+    // ---- selection length (CSA: the valid prefix of idx): a minimum per warp, joined below
     if (sel != nullptr) {
         int first_bad = a.k;
         for (int i = threadIdx.x; i < a.k; i += kTcThreads) {
             const int32_t v = __ldg(sel + i);
             if (v < 0 || v >= n) first_bad = min(first_bad, i);
-            if (v >= n) set_status(status, LCS_ERR_DEVICE, 603);
         }
         first_bad = __reduce_min_sync(0xffffffffu, first_bad);
-        if (lane == 0 && first_bad < a.k) atomicMin(&bars.nsel, first_bad);
-        __syncthreads();
-        nsel = bars.nsel;
-    } else {
-        nsel = (int)kv4_avail(a, g, n);
+        if (lane == 0) bars.first_bad[warp] = first_bad;
+    }
+    // ---- Q scaled by 2^e, content to fp16 unless window chunks come first, in the SW128 layout (column
+    // block c/8, 16-byte chunk c%8 of row h)
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        const int h = warp + kTcWarps * i;
+        if (h >= kH) continue;
+        uint32_t mag = 0;   // largest magnitude, as bf16 bits
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+            const uint32_t w[4] = {qv[i][c].x, qv[i][c].y, qv[i][c].z, qv[i][c].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mag = max(mag, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+        }
+        mag = __reduce_max_sync(0xffffffffu, mag);
+        const int ex = (int)(mag >> 7) - 127;               // of the largest element (subnormals: -127)
+        int e = mag == 0 || mag >= 0x7F80u ? 0 : 14 - ex;   // zero, infinite or NaN heads stay as they are
+        e = e > 126 ? 126 : e;
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        if (lane == 0) bars.qscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+            if (c == 2 && lane >= 8) continue;
+            const uint32_t w[4] = {qv[i][c].x, qv[i][c].y, qv[i][c].z, qv[i][c].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f0 = __uint_as_float(w[k] << 16) * up, f1 = __uint_as_float(w[k] & 0xFFFF0000u) * up;
+                o[k] = c < 2 && nwl == 0 ? pack_f16x2(f0, f1) : pack_bf16x2(f0, f1);
+            }
+            const int ch = c * 32 + lane;
+            *reinterpret_cast<uint4*>(q_s + (ch >> 3) * (kH * 128) + sw128_off(h, ch & 7)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)uni((int)bars.tmem_base);
+    int nsel = most;
+    if (sel != nullptr) {
+        for (int i = 0; i < kTcWarps; ++i) nsel = min(nsel, bars.first_bad[i]);
+        // an index past the entries ended it; -1 is the padding
+        if (threadIdx.x == 0 && nsel < a.k && __ldg(sel + nsel) >= 0) set_status(status, LCS_ERR_DEVICE, 603);
     }
     const int nch_all = nwc + (nsel + kChunk - 1) / kChunk;
-    const int nch = sp < nch_all ? (nch_all - sp + splits - 1) / splits : 0;      // this split's chunks
-    const int nwl = sp < nwc ? (nwc - sp + splits - 1) / splits : 0;              // window chunks among them, first
-    auto gcof = [&](int c) -> int { return sp + splits * c; };
+    const int nch = uni(sp < nch_all ? (nch_all - sp + splits - 1) / splits : 0);   // this split's chunks
     auto chunk_valid = [&](int gc) -> int {
         const int64_t v = gc < nwc ? wp.n - (int64_t)gc * kChunk : (int64_t)nsel - (int64_t)(gc - nwc) * kChunk;
         return (int)(v < kChunk ? v : kChunk);
     };
 
-    // ---- producers' first rows are on their way while every warp brings in Q
-    const bool producer = warp >= 4 && warp < 12;
-    const int pw = warp - 4;
-    const int r0 = pw * 8 + (lane >> 3);   // this lane's rows of a chunk: r0, r0 + 4
-    auto row_of = [&](int gc, int r) -> const uint8_t* {   // entry row r of compressed chunk gc, or null
-        const int j = (gc - nwc) * kChunk + r;
-        if (j >= nsel) return nullptr;
-        return kv4_row(a, b, sel != nullptr ? __ldg(sel + j) : j, status);
-    };
-    auto load_rows = [&](RawRows& x, const uint8_t* const (&src)[2]) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint8_t* p = src[i] + 16 * (lane & 7);
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                x.codes[hf][i] = make_uint4(0, 0, 0, 0);
-                x.scale[hf][i] = 0;
-                if (src[i] != nullptr) {
-                    x.codes[hf][i] = __ldg(reinterpret_cast<const uint4*>(p + 128 * hf));
-                    x.scale[hf][i] = __ldg(src[i] + 384 + 8 * hf + (lane & 7));
-                }
-            }
-            x.rope[i] = make_uint4(0, 0, 0, 0);
-            if (src[i] != nullptr) x.rope[i] = __ldg(reinterpret_cast<const uint4*>(p + 256));
-        }
-    };
-    RawRows raw;
-    const uint8_t* nxt[2] = {nullptr, nullptr};
-    if (producer && nwl < nch) {
-        const uint8_t* src[2] = {row_of(gcof(nwl), r0), row_of(gcof(nwl), r0 + 4)};
-        load_rows(raw, src);
-        if (nwl + 1 < nch) {
-            nxt[0] = row_of(gcof(nwl + 1), r0);
-            nxt[1] = row_of(gcof(nwl + 1), r0 + 4);
-        }
-    }
-    // ---- Q: warp w takes heads w, w + 14, ...; scaled by 2^e, content to fp16 unless window chunks
-    // come first, in the SW128 layout (column block c/8, 16-byte chunk c%8 of row h)
-    if (nch > 0) {
-        constexpr int kHeads = (kH + kTcWarps - 1) / kTcWarps;
-        uint4 v[kHeads][3];
-        const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (g * a.H + h0) * kD);
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i)
-#pragma unroll
-            for (int c = 0; c < 3; ++c) {
-                const int h = warp + kTcWarps * i;
-                v[i][c] = make_uint4(0, 0, 0, 0);
-                if (h < nh && (c < 2 || lane < 8)) v[i][c] = __ldg(qg + h * (kD / 8) + c * 32 + lane);
-            }
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-            const int h = warp + kTcWarps * i;
-            if (h >= kH) continue;
-            uint32_t mag = 0;   // largest magnitude, as bf16 bits
-#pragma unroll
-            for (int c = 0; c < 3; ++c) {
-                const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mag = max(mag, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-            }
-            mag = __reduce_max_sync(0xffffffffu, mag);
-            const int ex = (int)(mag >> 7) - 127;             // of the largest element (subnormals: -127)
-            int e = mag == 0 || mag >= 0x7F80u ? 0 : 14 - ex;   // zero, infinite or NaN heads stay as they are
-            e = e > 126 ? 126 : e;
-            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-            if (lane == 0) bars.qscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-            for (int c = 0; c < 3; ++c) {
-                if (c == 2 && lane >= 8) continue;
-                const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float f0 = __uint_as_float(w[k] << 16) * up, f1 = __uint_as_float(w[k] & 0xFFFF0000u) * up;
-                    o[k] = c < 2 && nwl == 0 ? pack_f16x2(f0, f1) : pack_bf16x2(f0, f1);
-                }
-                const int ch = c * 32 + lane;
-                *reinterpret_cast<uint4*>(q_s + (ch >> 3) * (kH * 128) + sw128_off(h, ch & 7)) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
-            }
-        }
-        fence_proxy_async_smem();
-    }
-    __syncthreads();
-
     constexpr uint32_t id_qk_b = idesc_bf16(64, kChunk, false, false), id_qk_h = idesc_f16(id_qk_b);
     constexpr uint32_t id_pv_b = idesc_bf16(64, 256, false, true), id_pv_h = idesc_f16(id_pv_b);
     auto t_s = [&](int buf) { return tmem + 256u + 64u * (uint32_t)buf; };
-    const uint32_t on = lane == 0 ? 1u : 0u;   // the issuing lane
 
     if (warp == kWarpQK) {
         // ---------------- Q.K^T issue
+        const uint32_t on = elect_lane();
         const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024);
-        const uint64_t k_desc0 = sw128_desc(smem_u32(stage_s), 16, 1024);
-        bool ok = true;
-        for (int c = 0; c < nch && ok; ++c) {
+        const uint32_t qa = (uint32_t)q_desc, hi = (uint32_t)(q_desc >> 32);
+        const uint32_t ka0 = (uint32_t)sw128_desc(smem_u32(stage_s), 16, 1024);
+        for (int c = 0; c < nch; ++c) {
             const int st = c & 1;
             if (nwl > 0 && c == nwl && !warp_wait(&bars.qconv, 0, status, 604)) break;
             if (c >= 2 && !warp_wait(&bars.sempty[st], (uint32_t)(((c - 2) >> 1) & 1), status, 605)) break;
-            const uint64_t kd = k_desc0 + (uint64_t)((st * kStageBytes) >> 4);
+            const uint32_t ka = ka0 + (uint32_t)((st * kStageBytes) >> 4);
             const uint32_t id = c < nwl ? id_qk_b : id_qk_h;
             if (!warp_wait(&bars.kfull[st][0], (uint32_t)((c >> 1) & 1), status, 606)) break;
             tc_fence_after();
 #pragma unroll
             for (int s = 0; s < 4 * kHalfBlocks; ++s)
-                mma_ss_if(on, t_s(st), q_desc + (uint64_t)(((s >> 2) * (kH * 128) + (s & 3) * 32) >> 4),
-                          kd + (uint64_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), id, s ? 1u : 0u);
+                mma_ss_if(on, t_s(st), qa + (uint32_t)(((s >> 2) * (kH * 128) + (s & 3) * 32) >> 4),
+                          ka + (uint32_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), hi, id, s ? 1u : 0u);
             if (!warp_wait(&bars.kfull[st][1], (uint32_t)((c >> 1) & 1), status, 607)) break;
             tc_fence_after();
 #pragma unroll
             for (int s = 4 * kHalfBlocks; s < 36; ++s)
-                mma_ss_if(on, t_s(st), q_desc + (uint64_t)(((s >> 2) * (kH * 128) + (s & 3) * 32) >> 4),
-                          kd + (uint64_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), s < 32 ? id : id_qk_b, 1u);
+                mma_ss_if(on, t_s(st), qa + (uint32_t)(((s >> 2) * (kH * 128) + (s & 3) * 32) >> 4),
+                          ka + (uint32_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), hi, s < 32 ? id : id_qk_b, 1u);
             commit_if(on, &bars.sfull[st]);
         }
     } else if (warp == kWarpPV) {
         // ---------------- P.V issue (its own warp: it never waits behind the next Q.K^T's rows)
-        const uint64_t k_desc0 = sw128_desc(smem_u32(stage_s), 16, 1024);
-        const uint64_t v_desc0 = sw128_desc(smem_u32(stage_s), kBlk, 1024);
+        const uint32_t on = elect_lane();
+        const uint64_t p_desc = sw128_desc(smem_u32(stage_s) + 8 * kBlk, 16, 1024);
+        const uint32_t pa0 = (uint32_t)p_desc, hi = (uint32_t)(p_desc >> 32);
+        const uint32_t va0 = (uint32_t)sw128_desc(smem_u32(stage_s), kBlk, 1024);
         for (int c = 0; c < nch; ++c) {
             const int st = c & 1;
             if (!warp_wait(&bars.pfull[st], (uint32_t)((c >> 1) & 1), status, 608)) break;
             tc_fence_after();
-            const uint64_t pd = k_desc0 + (uint64_t)((st * kStageBytes + 8 * kBlk) >> 4);
-            const uint64_t vd = v_desc0 + (uint64_t)((st * kStageBytes) >> 4);
+            const uint32_t pa = pa0 + (uint32_t)((st * kStageBytes) >> 4);
+            const uint32_t va = va0 + (uint32_t)((st * kStageBytes) >> 4);
             const uint32_t id = c < nwl ? id_pv_b : id_pv_h;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ss_if(on, tmem + (half ? (16u << 16) : 0u), pd + (uint64_t)((kk * 32) >> 4),
-                              vd + (uint64_t)((half * kHalfBlocks * kBlk + kk * 2048) >> 4), id, (c | kk) ? 1u : 0u);
+                    mma_ss_if(on, tmem + (half ? (16u << 16) : 0u), pa + (uint32_t)((kk * 32) >> 4),
+                              va + (uint32_t)((half * kHalfBlocks * kBlk + kk * 2048) >> 4), hi, id, (c | kk) ? 1u : 0u);
                 // dims 0-255 read column blocks 0-3; blocks 4-8 are released after the rest
                 commit_if(on, &bars.kempty[st][half]);
             }
@@ -533,21 +572,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint8_t* dst = stage_s + st * kStageBytes;
             const uint32_t par = (uint32_t)((((c >> 1) - 1)) & 1);
             if (c < nwl) {
-                // window chunk: bf16 rows by 16-byte cp.async, zeros past the last row
                 if (c >= 2 && (!warp_wait(&bars.kempty[st][0], par, status, 609) ||
                                !warp_wait(&bars.kempty[st][1], par, status, 610)))
                     break;
-                const int gc = gcof(c), nv = chunk_valid(gc);
-                const uint8_t* w0 = static_cast<const uint8_t*>(a.win) +
-                                    (b * a.Tw + wp.lo + (int64_t)gc * kChunk) * (kD * 2);
-                for (int i = 0; i < 8; ++i) {
-                    const int r = pw * 8 + i;
-                    const bool valid = r < nv;
-                    for (int ch = lane; ch < 72; ch += 32)
-                        cp_async_16(dst + (ch >> 3) * kBlk + sw128_off(r, ch & 7), w0 + (valid ? r * (kD * 2) + ch * 16 : 0),
-                                    valid);
-                }
-                cp_async_commit();
+                if (c > 0) load_window(c);   // the first is on its way
                 cp_async_wait<0>();
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -557,6 +585,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 continue;
             }
+            const bool attended = my_row < chunk_valid(gcof(c));
+            if (attended && cur == nullptr) set_status(status, LCS_ERR_DEVICE, 602);
+            const bool live = attended && cur != nullptr;
             bool ok = true;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -564,20 +595,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ok = false;
                     break;
                 }
+                // piece p = (lane >> 3) + 4 i: codes 32 p .. 32 p + 31, 16-byte chunks 4 (p & 1) .. + 3 of column
+                // block p / 2.  A store's eight lanes hold eight rows: eight bank groups.
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = r0 + 4 * i;
-                    const uint32_t s2 = scale_f16x2(raw.scale[hf][i]);
-                    const uint4 cv = raw.codes[hf][i];
-                    // codes 32 p .. 32 p + 31 of the row, p = 8 hf + (lane & 7): chunks 4 (p & 1) + 0..3 of block p / 2
-                    uint8_t* blk = dst + (4 * hf + ((lane & 7) >> 1)) * kBlk;
+                for (int i = 2 * hf; i < 2 * hf + 2; ++i) {
+                    const uint32_t sw = i == 0 ? raw.scales.x : i == 1 ? raw.scales.y : i == 2 ? raw.scales.z : raw.scales.w;
+                    const uint32_t s2 = live ? scale_f16x2(sw, lane >> 3) : 0u;
+                    const uint4 cv = live ? raw.codes[i] : make_uint4(0, 0, 0, 0);
+                    const int p = (lane >> 3) + 4 * i;
+                    uint8_t* blk = dst + (p >> 1) * kBlk;
+                    const int ch = 4 * (p & 1);
+                    *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch)) = widen8_cvt(cv.x, s2);
+                    *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 1)) = widen8_perm(cv.y, s2);
+                    *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 2)) = widen8_cvt(cv.z, s2);
+                    *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 3)) = widen8_perm(cv.w, s2);
+                }
+                if (hf) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int q = (k + ((lane & 7) >> 1)) & 3;
-                        const uint32_t w = q & 2 ? (q & 1 ? cv.w : cv.z) : (q & 1 ? cv.y : cv.x);
-                        *reinterpret_cast<uint4*>(blk + sw128_off(r, 4 * (lane & 1) + q)) = widen8(w, s2);
-                    }
-                    if (hf) *reinterpret_cast<uint4*>(dst + 8 * kBlk + sw128_off(r, lane & 7)) = raw.rope[i];
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<uint4*>(dst + 8 * kBlk + sw128_off(my_row, (lane >> 3) + 4 * i)) =
+                            live ? raw.rope[i] : make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -585,14 +622,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (!ok) break;
             // the next chunk's rows into the registers, and where the one after lies
-            if (c + 1 < nch) {
-                load_rows(raw, nxt);
-                if (c + 2 < nch) {
-                    nxt[0] = row_of(gcof(c + 2), r0);
-                    nxt[1] = row_of(gcof(c + 2), r0 + 4);
-                }
-            }
+            cur = nxt;
+            if (c + 1 < nch) load_row(cur);
+            if (c + 2 < nch) nxt = row_of(c + 2);
         }
+        cp_async_wait<0>();
     } else if (warp < 4) {
         // ---------------- softmax: warp q owns heads 16q..16q+15; lane l works on head 16q + (l & 15), on
         // S columns 0-31 (lanes 0-15) or 32-63 (lanes 16-31)
@@ -600,6 +634,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int cbase = (lane < 16) ? 0 : 32;
         float m_used = -INFINITY, l_sum = 0.f;   // log2 domain; weights are 2^(s - m_used + kLift)
         const float sl2 = nch > 0 ? a.scale * kLog2e * bars.qscale[head] : 0.f;
+        const uint32_t flip = sl2 < 0.f ? 0x80000000u : 0u;
         for (int c = 0; c < nch; ++c) {
             const int st = c & 1;
             const bool wchunk = c < nwl;
@@ -625,12 +660,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tmem_ld_wait();
             tc_fence_before();
             mbar_arrive(&bars.sempty[st]);
-            const int nv = chunk_valid(gcof(c)) - cbase;   // this lane's valid columns
+            const int valid = chunk_valid(gcof(c));
+            // the maximum of scale * s is that of s (of -s for a negative scale) times |scale|
             float mx = -INFINITY;
+            if (valid == kChunk) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < nv) mx = fmaxf(mx, __uint_as_float(sv[j]) * sl2);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(sv[j] ^ flip));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (cbase + j < valid) mx = fmaxf(mx, __uint_as_float(sv[j] ^ flip));
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * fabsf(sl2);
             float alpha = 1.f;
             bool rescale = false;
             if (mx > m_used + kRescale || m_used == -INFINITY) {
@@ -641,20 +682,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             const float off = m_used == -INFINITY ? 0.f : m_used - kLift;   // every score -inf: weights 0
             uint8_t* pblk = stage_s + st * kStageBytes + 8 * kBlk;
-            float psum = 0.f;
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                uint32_t pk[4];
+            for (int j = 0; j < 32; ++j) sv[j] = __float_as_uint(ex2(fmaf(__uint_as_float(sv[j]), sl2, -off)));
+            if (valid < kChunk) {   // columns past the chunk's rows weigh nothing
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int j = ch * 8 + 2 * q;
-                    const float p0 = j < nv ? exp2f(__uint_as_float(sv[j]) * sl2 - off) : 0.f;
-                    const float p1 = j + 1 < nv ? exp2f(__uint_as_float(sv[j + 1]) * sl2 - off) : 0.f;
-                    pk[q] = wchunk ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
-                    psum += p0 + p1;
-                }
-                *reinterpret_cast<uint4*>(pblk + sw128_off(head, (cbase >> 3) + ch)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                for (int j = 0; j < 32; ++j)
+                    if (cbase + j >= valid) sv[j] = 0u;
             }
+            float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 32; ++j) ps[j & 3] += __uint_as_float(sv[j]);
+            float psum = (ps[0] + ps[1]) + (ps[2] + ps[3]);
+            if (wchunk) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sv[j] = pack_bf16x2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sv[j] = pack_f16x2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1]));
+            }
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+                *reinterpret_cast<uint4*>(pblk + sw128_off(head, (cbase >> 3) + ch)) =
+                    make_uint4(sv[4 * ch], sv[4 * ch + 1], sv[4 * ch + 2], sv[4 * ch + 3]);
             psum += __shfl_xor_sync(0xffffffffu, psum, 16);
             l_sum = l_sum * alpha + psum;
             if (__any_sync(0xffffffffu, rescale)) {
@@ -677,9 +726,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             fence_proxy_async_smem();
             mbar_arrive(&bars.pfull[st]);
         }
-        // ---- O (normalised when this is the only split; else the partial O and (m, l)) staged through
-        // shared memory.  Lane l of warp q holds the O row of head 16q + (l & 15), dims 0-255 (lanes
-        // 0-15) or 256-511 (lanes 16-31).
+        // ---- O.  Lane l of warp q holds the O row of head 16q + (l & 15), dims 0-255 (lanes 0-15) or 256-511
+        // (lanes 16-31).  The only split: normalised, staged through shared memory.  One of several: the
+        // partial and (m, l), for the cluster's merge staged in fp32, else written as the lanes hold it
+        // ([quarter][4 dims][lane], 512 bytes a store).
         if (nch > 0) warp_wait(&bars.odone, 0, status, 622);
         tc_fence_after();
         const bool final_out = splits == 1;
@@ -687,6 +737,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int dim0 = (lane < 16) ? 0 : 256;
         const bool f32 = !final_out || a.out_dtype == LCS_F32;
         uint8_t* rowp = stage_s + head * (f32 ? kOPitchF32 : kOPitchBF16);
+        float4* gpart = reinterpret_cast<float4*>(part_o) + ((int64_t)(unit * splits + sp) * 4 + warp) * (64 * 32) + lane;
         for (int j0 = 0; j0 < 256 / 16; j0 += 4) {
             uint32_t ov[4][16];
             if (nch > 0) {
@@ -704,10 +755,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int j = j0 + u;
                 if (f32) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        reinterpret_cast<float4*>(rowp + (dim0 + j * 16) * 4)[q] =
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 v =
                             make_float4(__uint_as_float(ov[u][4 * q]) * fs, __uint_as_float(ov[u][4 * q + 1]) * fs,
                                         __uint_as_float(ov[u][4 * q + 2]) * fs, __uint_as_float(ov[u][4 * q + 3]) * fs);
+                        if (final_out || cmerge) reinterpret_cast<float4*>(rowp + (dim0 + j * 16) * 4)[q] = v;
+                        else __stcg(gpart + (4 * j + q) * 32, v);
+                    }
                 } else {
                     uint32_t pk[8];
 #pragma unroll
@@ -722,9 +776,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const float m = l_sum > 0.f ? m_used - kLift : -INFINITY;
             if (final_out) {
                 if (a.lse != nullptr && head < nh)
-                    a.lse[g * a.H + h0 + head] = l_sum > 0.f ? (m + log2f(l_sum)) / kLog2e : -INFINITY;
+                    a.lse[(int64_t)g * a.H + h0 + head] = l_sum > 0.f ? (m + log2f(l_sum)) / kLog2e : -INFINITY;
             } else {
-                float* ml = cmerge ? ml_s + 2 * head : part_ml + ((unit * splits + sp) * kH + head) * 2;
+                float* ml = cmerge ? ml_s + 2 * head : part_ml + ((int64_t)(unit * splits + sp) * kH + head) * 2;
                 ml[0] = m;
                 ml[1] = l_sum;
             }
@@ -757,7 +811,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 Ls += l * f;
             }
             wt[threadIdx.x * kW + kMaxCluster] = Ls > 0.f ? 1.f / Ls : 0.f;
-            if (a.lse != nullptr) a.lse[g * a.H + h0 + h] = Ls > 0.f ? (M + log2f(Ls)) / kLog2e : -INFINITY;
+            if (a.lse != nullptr) a.lse[(int64_t)g * a.H + h0 + h] = Ls > 0.f ? (M + log2f(Ls)) / kLog2e : -INFINITY;
         }
         __syncthreads();
         for (int it = (int)threadIdx.x; it < nm * (kDv / 4); it += kTcThreads) {
@@ -775,7 +829,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 acc.w += v.w * f;
             }
             const float iv = rw[kMaxCluster];
-            const int64_t o4 = (g * a.H + h0 + h) * (kDv / 4) + q4;
+            const int64_t o4 = ((int64_t)g * a.H + h0 + h) * (kDv / 4) + q4;
             if (a.out_dtype == LCS_F32)
                 reinterpret_cast<float4*>(a.out)[o4] = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
             else
@@ -783,15 +837,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     make_uint2(pack_bf16x2(acc.x * iv, acc.y * iv), pack_bf16x2(acc.z * iv, acc.w * iv));
         }
         cluster_sync_all();   // no CTA leaves while a peer still reads its staged partial
-    } else {
-        // the staged rows (the output's heads, or this split's partial) with coalesced 16-byte stores
-        const bool f32 = splits > 1 || a.out_dtype == LCS_F32;
+    } else if (splits == 1) {
+        // the staged output rows with coalesced 16-byte stores
+        const bool f32 = a.out_dtype == LCS_F32;
         const int pitch = f32 ? kOPitchF32 : kOPitchBF16;
         const int rb = f32 ? kDv * 4 : kDv * 2;
-        uint8_t* gout = splits == 1 ? static_cast<uint8_t*>(a.out) + (g * a.H + h0) * rb
-                                    : reinterpret_cast<uint8_t*>(part_o + (unit * splits + sp) * kH * kDv);
-        const int rows = splits == 1 ? nh : kH;
-        for (int off = (int)threadIdx.x * 16; off < rows * rb; off += kTcThreads * 16) {
+        uint8_t* gout = static_cast<uint8_t*>(a.out) + ((int64_t)g * a.H + h0) * rb;
+        for (int off = (int)threadIdx.x * 16; off < nh * rb; off += kTcThreads * 16) {
             const int h = off / rb, cb = off - h * rb;
             *reinterpret_cast<uint4*>(gout + off) = *reinterpret_cast<const uint4*>(stage_s + h * pitch + cb);
         }
@@ -805,69 +857,85 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
 }
 
-// Merges the split partials of one (query, head) per CTA: 128 threads, one float4 of the 512 output
-// dims each; weights 2^(m_s - M) and 1/L formed once; sums in split order, eight loads at a time.
-__global__ void __launch_bounds__(128) kv4_combine_kernel(const float* __restrict__ part_o,
-                                                          const float* __restrict__ part_ml, int splits, int H, int tiles,
-                                                          void* __restrict__ out, int out_dtype, float* __restrict__ lse) {
-    __shared__ float fac[kMaxSplits];
-    __shared__ float inv_l;
-    const int64_t gh = blockIdx.x;   // query * H + head
-    const int64_t g = gh / H;
-    const int hh = (int)(gh - g * H), t = threadIdx.x;
-    const int64_t unit = g * tiles + hh / kH;
-    const int h = hh % kH;
+// Merges the split partials.  A CTA (8 warps) takes 16 heads of one unit (quarter = the softmax warp
+// that wrote them) and 32 dims of either half: a warp's lanes read 512 bytes of each split as they
+// were written, in split order, eight splits in flight; the weights 2^(m_s - M) and 1/L come from
+// one warp per two heads; the results go out through shared memory, 32 dims of a head together.
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads)
+    kv4_merge_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml, int splits, int H, int tiles,
+                     void* __restrict__ out, int out_dtype, float* __restrict__ lse) {
+    __shared__ float fac[16][kMaxSplits + 1];
+    __shared__ float inv_l[16];
+    __shared__ float o_s[32][33];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int part = blockIdx.x & 7, quarter = (blockIdx.x >> 3) & 3;   // dims 32 part .. + 31 of both halves
+    const int unit = blockIdx.x >> 5;
+    const int g = tiles == 2 ? unit >> 1 : unit, h0 = (tiles == 2 ? (unit & 1) * kH : 0) + 16 * quarter;
 #if defined(__CUDA_ARCH__)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 #endif
-    if (t < 32) {
+    if (h0 >= H) return;
+    for (int i = 2 * warp; i < 2 * warp + 2; ++i) {
         float2 ml[2];
         float M = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int s = t + 32 * i;
-            ml[i] = make_float2(-INFINITY, 0.f);
-            if (s < splits) ml[i] = __ldcg(reinterpret_cast<const float2*>(part_ml) + (unit * splits + s) * kH + h);
-            M = fmaxf(M, ml[i].x);
+        for (int k = 0; k < 2; ++k) {
+            const int s = lane + 32 * k;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (s < splits)
+                ml[k] = __ldcg(reinterpret_cast<const float2*>(part_ml) + ((int64_t)unit * splits + s) * kH + 16 * quarter + i);
+            M = fmaxf(M, ml[k].x);
         }
         M = warp_max(M);
         float L = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float e = ml[i].y > 0.f ? exp2f(ml[i].x - M) : 0.f;
-            if (t + 32 * i < splits) fac[t + 32 * i] = e;
-            L += ml[i].y * e;
+        for (int k = 0; k < 2; ++k) {
+            const float e = ml[k].y > 0.f ? exp2f(ml[k].x - M) : 0.f;
+            if (lane + 32 * k < splits) fac[i][lane + 32 * k] = e;
+            L += ml[k].y * e;
         }
         L = warp_sum(L);   // a fixed tree
-        if (t == 0) {
-            inv_l = L > 0.f ? 1.f / L : 0.f;
-            if (lse != nullptr) lse[gh] = L > 0.f ? (M + log2f(L)) / kLog2e : -INFINITY;
+        if (lane == 0) {
+            inv_l[i] = L > 0.f ? 1.f / L : 0.f;
+            if (lse != nullptr && part == 0 && h0 + i < H)
+                lse[(int64_t)g * H + h0 + i] = L > 0.f ? (M + log2f(L)) / kLog2e : -INFINITY;
         }
     }
     __syncthreads();
-    const float4* src = reinterpret_cast<const float4*>(part_o) + (unit * splits * kH + h) * (kDv / 4) + t;
+    const float4* src = reinterpret_cast<const float4*>(part_o) +
+                        (((int64_t)unit * splits * 4 + quarter) * 64 + 8 * part + warp) * 32 + lane;
+    const int i = lane & 15;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = 0; s0 < splits; s0 += 8) {
         float4 v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (s0 + i < splits) v[i] = __ldcg(src + (int64_t)(s0 + i) * kH * (kDv / 4));
+        for (int k = 0; k < 8; ++k)
+            if (s0 + k < splits) v[k] = __ldcg(src + (int64_t)(s0 + k) * (4 * 64 * 32));
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (s0 + i < splits) {
-                const float e = fac[s0 + i];
-                acc.x += v[i].x * e;
-                acc.y += v[i].y * e;
-                acc.z += v[i].z * e;
-                acc.w += v[i].w * e;
+        for (int k = 0; k < 8; ++k)
+            if (s0 + k < splits) {
+                const float e = fac[i][s0 + k];
+                acc.x += v[k].x * e;
+                acc.y += v[k].y * e;
+                acc.z += v[k].z * e;
+                acc.w += v[k].w * e;
             }
     }
-    const float iv = inv_l;
-    if (out_dtype == LCS_F32)
-        reinterpret_cast<float4*>(out)[gh * (kDv / 4) + t] = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
-    else
-        reinterpret_cast<uint2*>(out)[gh * (kDv / 4) + t] =
-            make_uint2(pack_bf16x2(acc.x * iv, acc.y * iv), pack_bf16x2(acc.z * iv, acc.w * iv));
+    const float iv = inv_l[i];
+    o_s[lane][4 * warp] = acc.x * iv;
+    o_s[lane][4 * warp + 1] = acc.y * iv;
+    o_s[lane][4 * warp + 2] = acc.z * iv;
+    o_s[lane][4 * warp + 3] = acc.w * iv;
+    __syncthreads();
+    // row r of o_s: head r & 15, dims (r < 16 ? 0 : 256) + 32 part + column
+    const int r = t >> 3, c4 = (t & 7) * 4;
+    if (h0 + (r & 15) < H) {
+        const int64_t at = ((int64_t)g * H + h0 + (r & 15)) * kDv + (r < 16 ? 0 : 256) + 32 * part + c4;
+        const float x = o_s[r][c4], y = o_s[r][c4 + 1], z = o_s[r][c4 + 2], w = o_s[r][c4 + 3];
+        if (out_dtype == LCS_F32) *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(x, y, z, w);
+        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
+    }
 }
 
 bool use_tc(const AttendKv4Args& a) { return a.q_dtype == LCS_BF16 && a.d_c == kDv && a.d_r == kD - kDv; }
@@ -937,7 +1005,7 @@ cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaSt
     }
     const int cmerge = kv4_cluster_ok(splits, units) ? 1 : 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * splits));
+    cfg.gridDim = splits > 1 ? dim3((unsigned)splits, (unsigned)units) : dim3((unsigned)units);
     cfg.blockDim = dim3(kTcThreads);
     cfg.dynamicSmemBytes = kTcSmem;
     cfg.stream = s;
@@ -950,8 +1018,8 @@ cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaSt
     cfg.numAttrs = cmerge;
     e = cudaLaunchKernelEx(&cfg, attend_kv4_tc_kernel, a, tiles, splits, cmerge, part_o, part_ml, status);
     if (e != cudaSuccess || splits == 1 || cmerge) return e;
-    return launch_k(kv4_combine_kernel, dim3((unsigned)(a.B * a.Q * a.H)), dim3(128), 0, s, true, part_o, part_ml, splits,
-                    a.H, tiles, a.out, a.out_dtype, a.lse);
+    return launch_k(kv4_merge_kernel, dim3((unsigned)(units * 32)), dim3(kMergeThreads), 0, s, true, part_o, part_ml,
+                    splits, a.H, tiles, a.out, a.out_dtype, a.lse);
 }
 
 }  // namespace
