@@ -206,8 +206,9 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
 //    content dims of Q are fp16 too, scaled per head by a power of two that puts the head's largest
 //    element in [2^14, 2^15) (exact down to 2^-28 of it, below that off by 2^-39 of it), and P is fp16
 //    (11 bits; 2^-11 a weight, against 2^-8 of bf16).  RoPE dims stay bf16: four MMAs of the same
-//    accumulation.  Window rows are bf16 of any size: their chunks come first, with all of Q in
-//    bf16 (scaled by the same powers of two) and P in bf16; Q's content is then converted in place.
+//    accumulation.  Window rows' content goes from bf16 to fp16 as well: exact from 2^-14 to 65504
+//    (their bf16 has 8 bits), off by 2^-25 below, where 4-bit rows resolve 2^-10, and saturating
+//    above, where 4-bit rows end at 2688.
 //  * A chunk's 64 widened rows (72 KB) are the K-major B of Q.K^T and the MN-major B of P.V;
 //    two stages, each released in two halves of the columns as P.V leaves them.  Warps 4-11
 //    fill: a warp owns 8 rows and holds the next chunk's 400-byte rows in registers (six 16-byte loads
@@ -225,17 +226,18 @@ constexpr int kH = 64, kD = 576, kDv = 512, kChunk = 64;
 constexpr int kBlk = kChunk * 128;            // one SW128 column block of a chunk: 64 rows x 128 B
 constexpr int kStageBytes = 9 * kBlk;         // 72 KB
 constexpr int kQBytes = 9 * (kH * 128);       // 72 KB
-constexpr int kTcThreads = 448, kTcWarps = 14;
-constexpr int kWarpQK = 12, kWarpPV = 13;
-constexpr int kProdWarps = 8;
+constexpr int kSoftWarps = 4, kProdWarps = 8;
+constexpr int kWarpQK = kSoftWarps + kProdWarps, kWarpPV = kWarpQK + 1, kTcWarps = kWarpPV + 1;
+constexpr int kTcThreads = kTcWarps * 32;
+constexpr int kRowsPerWarp = kChunk / kProdWarps;             // rows of a chunk per producer warp
+constexpr int kPieces = 32 / kRowsPerWarp;                    // lanes that share a row
+static_assert(kRowsPerWarp == 4 || kRowsPerWarp == 8, "a store's eight lanes meet eight bank groups");
 constexpr int kHalfBlocks = 4;                // column blocks of a stage's first half
 constexpr size_t kTcSmem = 1024 + kQBytes + 2 * kStageBytes;
 constexpr int kMaxSplits = 64;
-constexpr int kMaxCluster = 8;
 constexpr int kOPitchF32 = kDv * 4 + 16;      // staged O rows (padded)
 constexpr int kOPitchBF16 = kDv * 2 + 16;
-static_assert(kH * kOPitchF32 + 4 * (2 * kH + kH / 2 * (kMaxCluster + 2)) <= 2 * kStageBytes,
-              "staged O, (m, l) and the merge weights fit in the stages");
+static_assert(kH * kOPitchF32 <= 2 * kStageBytes, "staged O fits in the stages");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.0f;              // log2 of the tolerated growth before O is rescaled
 constexpr float kLift = 6.0f;                 // log2 of the largest weight when the maximum is current
@@ -246,7 +248,6 @@ struct TcBars {
     uint64_t pfull[2];
     uint64_t ofull[2];                        // P.V of chunk c done (per chunk parity)
     uint64_t odone;                           // every P.V of this CTA done
-    uint64_t qconv;                           // Q's content is fp16 now
     uint32_t tmem_base;
     int first_bad[kTcWarps];
     float qscale[kH];                         // 2^-e of head h: the true q is the stored one times it
@@ -284,9 +285,31 @@ __device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
 // The same instruction descriptor with fp16 operands.
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t bf16) { return bf16 & ~((1u << 7) | (1u << 10)); }
 
-// A bounded wait that the whole warp leaves with one answer.
+// A bounded wait that the whole warp leaves with one answer.  The thread sleeps in the hardware's wait
+// (up to the hint, 20 us) instead of polling: two dozen polling warps took the issue slots of the
+// few that had work.  The clock and the grid's status word are looked at after every 16 sleeps.
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int where) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, where));
+    uint64_t t0 = 0;
+    for (uint32_t polls = 1;; ++polls) {
+        if (__all_sync(0xffffffffu, mbar_sleep(bar, parity))) return true;
+        if (polls & 15u) continue;
+        const uint64_t now = globaltimer();
+        if (t0 == 0) t0 = now;
+        const bool late = now - t0 > kWaitBudgetNs;
+        if (late) set_status(status, LCS_ERR_TIMEOUT, where);
+        if (__any_sync(0xffffffffu, late || *(volatile int*)status != 0)) return false;
+    }
 }
 
 __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
@@ -303,6 +326,12 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+// Two bf16 -> two fp16: exact from 2^-14 to 65504, where it saturates; below off by 2^-25 at most.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(w & 0xFFFF0000u)), "f"(__uint_as_float(w << 16)));
     return r;
 }
 // Eight E2M1 codes (low nibble first) times the scale (in both halves) -> eight fp16, exact.  Two
@@ -338,21 +367,20 @@ __device__ __forceinline__ uint32_t scale_f16x2(uint32_t w, int at) {
     return r;
 }
 
-// A lane's part of row lane & 7 of its warp's eight rows of a chunk: the 16-byte pieces p = (lane >> 3)
-// + 4 i of the codes (i < 4) and of the RoPE dims (i < 2), and the row's scales.
+// A lane's part of row lane % kRowsPerWarp of its warp's rows of a chunk: the 16-byte pieces p =
+// lane / kRowsPerWarp + kPieces i of the 16 of codes and the 8 of RoPE dims, and the row's scales.
 struct RawRow {
-    uint4 codes[4], rope[2], scales;
+    uint4 codes[16 / kPieces], rope[8 / kPieces], scales;
 };
 
 __global__ void __launch_bounds__(kTcThreads, 1)
-    attend_kv4_tc_kernel(const AttendKv4Args a, int tiles, int splits, int cmerge, float* __restrict__ part_o,
+    attend_kv4_tc_kernel(const AttendKv4Args a, int tiles, int splits, float* __restrict__ part_o,
                          float* __restrict__ part_ml, int* status) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ TcBars bars;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* q_s = smem;
     uint8_t* stage_s = smem + kQBytes;
-    float* ml_s = reinterpret_cast<float*>(stage_s + kH * kOPitchF32);   // (m, l) beside the staged O
 
     // values that steer whole warps come from lane 0, so that the compiler keeps them (and what the MMA
     // issue derives from them) in uniform registers
@@ -364,22 +392,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int h0 = tiles == 2 ? (unit & 1) * kH : 0;
     const int nh = min(kH, a.H - h0);
     const int b = a.Q == 1 ? g : (int)((unsigned)g / (unsigned)a.Q);
-    const bool producer = warp >= 4 && warp < 12;
-    const int pw = warp - 4;
+    const bool producer = warp >= kSoftWarps && warp < kWarpQK;
+    const int pw = warp - kSoftWarps;
 
-    // ---- the loads that nothing waits for, before everything else: Q (warp w takes heads w, w + 14, ...) ...
-    constexpr int kHeads = (kH + kTcWarps - 1) / kTcWarps;
-    uint4 qv[kHeads][3];
-    {
-        const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + ((int64_t)g * a.H + h0) * kD);
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i)
-#pragma unroll
-            for (int c = 0; c < 3; ++c) {
-                const int h = warp + kTcWarps * i;
-                qv[i][c] = make_uint4(0, 0, 0, 0);
-                if (h < nh && (c < 2 || lane < 8)) qv[i][c] = __ldg(qg + h * (kD / 8) + c * 32 + lane);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            for (int hf = 0; hf < 2; ++hf) {
+                mbar_init(&bars.kfull[i][hf], kProdWarps);
+                mbar_init(&bars.kempty[i][hf], 1);
             }
+            mbar_init(&bars.pfull[i], kSoftWarps);
+            mbar_init(&bars.sfull[i], 1);
+            mbar_init(&bars.sempty[i], kSoftWarps);
+            mbar_init(&bars.ofull[i], 1);
+        }
+        mbar_init(&bars.odone, 1);
+        fence_barrier_init();
+    }
+    if (warp == kWarpQK) {
+        tmem_alloc(&bars.tmem_base, 512);
+        tmem_relinquish();
+    }
+#if defined(__CUDA_ARCH__)
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // everything above reads no memory of the call
+#endif
+    // ---- the loads that nothing waits for, before everything else: Q as it is, in the SW128 layout (16-byte
+    // chunk c of head h: column block c / 8) ...
+    {
+        const uint8_t* qg = static_cast<const uint8_t*>(a.q) + ((int64_t)g * a.H + h0) * (kD * 2);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < kH * 72; i += kTcThreads) {
+            const int h = i / 72, c = i - h * 72;
+            cp_async_16(q_s + (c >> 3) * (kH * 128) + sw128_off(h, c & 7), qg + (h < nh ? i * 16 : 0), h < nh);
+        }
+        cp_async_commit();
     }
     // ... and the producers' first rows.  Which of a chunk's rows are attended is known later (the
     // selection's length): rows behind it are dropped when they are widened.
@@ -390,7 +436,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int32_t* sel = a.idx != nullptr ? a.idx + (int64_t)g * a.k : nullptr;
     const int most = sel != nullptr ? a.k : (int)kv4_avail(a, g, n);
     auto gcof = [&](int c) -> int { return sp + splits * c; };
-    const int my_row = pw * 8 + (lane & 7);
+    const int my_row = pw * kRowsPerWarp + lane % kRowsPerWarp, my_piece = lane / kRowsPerWarp;
     auto row_of = [&](int c) -> const uint8_t* {   // this lane's row of local chunk c, null if there is none
         const int j = (gcof(c) - nwc) * kChunk + my_row;
         if (j >= most) return nullptr;
@@ -399,12 +445,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     RawRow raw;
     auto load_row = [&](const uint8_t* src) {
-        const uint4* p = reinterpret_cast<const uint4*>(src) + (lane >> 3);
+        const uint4* p = reinterpret_cast<const uint4*>(src) + my_piece;
         if (src != nullptr) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) raw.codes[i] = __ldg(p + 4 * i);
-            raw.rope[0] = __ldg(p + 16);
-            raw.rope[1] = __ldg(p + 20);
+            for (int i = 0; i < 16 / kPieces; ++i) raw.codes[i] = __ldg(p + kPieces * i);
+#pragma unroll
+            for (int i = 0; i < 8 / kPieces; ++i) raw.rope[i] = __ldg(p + 16 + kPieces * i);
             raw.scales = __ldg(reinterpret_cast<const uint4*>(src) + 24);
         }
     };
@@ -413,8 +459,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint8_t* dst = stage_s + (c & 1) * kStageBytes;
         const int64_t w0 = (int64_t)gcof(c) * kChunk;
         const uint8_t* src = static_cast<const uint8_t*>(a.win) + ((int64_t)b * a.Tw + wp.lo + w0) * (kD * 2);
-        for (int i = 0; i < 8; ++i) {
-            const int r = pw * 8 + i;
+#pragma unroll 1
+        for (int i = 0; i < kRowsPerWarp; ++i) {
+            const int r = pw * kRowsPerWarp + i;
             const bool valid = w0 + r < wp.n;
             for (int ch = lane; ch < 72; ch += 32)
                 cp_async_16(dst + (ch >> 3) * kBlk + sw128_off(r, ch & 7), src + (valid ? r * (kD * 2) + ch * 16 : 0), valid);
@@ -429,25 +476,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         nxt = row_of(nwl + 1);
     }
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            for (int hf = 0; hf < 2; ++hf) {
-                mbar_init(&bars.kfull[i][hf], kProdWarps);
-                mbar_init(&bars.kempty[i][hf], 1);
-            }
-            mbar_init(&bars.pfull[i], 128);
-            mbar_init(&bars.sfull[i], 1);
-            mbar_init(&bars.sempty[i], 128);
-            mbar_init(&bars.ofull[i], 1);
-        }
-        mbar_init(&bars.odone, 1);
-        mbar_init(&bars.qconv, 128);
-        fence_barrier_init();
-    }
-    if (warp == kWarpQK) {
-        tmem_alloc(&bars.tmem_base, 512);
-        tmem_relinquish();
-    }
     // ---- selection length (CSA: the valid prefix of idx): a minimum per warp, joined below
     if (sel != nullptr) {
         int first_bad = a.k;
@@ -458,39 +486,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         first_bad = __reduce_min_sync(0xffffffffu, first_bad);
         if (lane == 0) bars.first_bad[warp] = first_bad;
     }
-    // ---- Q scaled by 2^e, content to fp16 unless window chunks come first, in the SW128 layout (column
-    // block c/8, 16-byte chunk c%8 of row h)
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        const int h = warp + kTcWarps * i;
-        if (h >= kH) continue;
-        uint32_t mag = 0;   // largest magnitude, as bf16 bits
+    cp_async_wait<0>();
+    __syncthreads();
+    // ---- Q scaled by 2^e in place, a warp per head; content to fp16
+#pragma unroll 1
+    for (int h = warp; h < kH; h += kTcWarps) {
+        uint8_t* qh = q_s + (lane >> 3) * (kH * 128) + sw128_off(h, lane & 7);   // chunks lane, lane + 32, lane + 64
+        uint4 v[3];
+        v[0] = *reinterpret_cast<const uint4*>(qh);
+        v[1] = *reinterpret_cast<const uint4*>(qh + 4 * (kH * 128));
+        v[2] = make_uint4(0, 0, 0, 0);
+        if (lane < 8) v[2] = *reinterpret_cast<const uint4*>(qh + 8 * (kH * 128));
+        uint32_t mag2 = 0;   // largest magnitudes of the even and odd elements, as bf16 bits
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
-            const uint32_t w[4] = {qv[i][c].x, qv[i][c].y, qv[i][c].z, qv[i][c].w};
+            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mag = max(mag, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+            for (int k = 0; k < 4; ++k) mag2 = __vmaxu2(mag2, w[k] & 0x7FFF7FFFu);
         }
-        mag = __reduce_max_sync(0xffffffffu, mag);
+        const uint32_t mag = __reduce_max_sync(0xffffffffu, max(mag2 & 0xFFFFu, mag2 >> 16));
         const int ex = (int)(mag >> 7) - 127;               // of the largest element (subnormals: -127)
         int e = mag == 0 || mag >= 0x7F80u ? 0 : 14 - ex;   // zero, infinite or NaN heads stay as they are
         e = e > 126 ? 126 : e;
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
         if (lane == 0) bars.qscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int c = 0; c < 3; ++c) {
-            if (c == 2 && lane >= 8) continue;
-            const uint32_t w[4] = {qv[i][c].x, qv[i][c].y, qv[i][c].z, qv[i][c].w};
+        auto scaled = [&](uint4 x, bool half) {
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
             uint32_t o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float f0 = __uint_as_float(w[k] << 16) * up, f1 = __uint_as_float(w[k] & 0xFFFF0000u) * up;
-                o[k] = c < 2 && nwl == 0 ? pack_f16x2(f0, f1) : pack_bf16x2(f0, f1);
+                o[k] = half ? pack_f16x2(f0, f1) : pack_bf16x2(f0, f1);
             }
-            const int ch = c * 32 + lane;
-            *reinterpret_cast<uint4*>(q_s + (ch >> 3) * (kH * 128) + sw128_off(h, ch & 7)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-        }
+            return make_uint4(o[0], o[1], o[2], o[3]);
+        };
+        *reinterpret_cast<uint4*>(qh) = scaled(v[0], true);
+        *reinterpret_cast<uint4*>(qh + 4 * (kH * 128)) = scaled(v[1], true);
+        if (lane < 8) *reinterpret_cast<uint4*>(qh + 8 * (kH * 128)) = scaled(v[2], false);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -511,7 +543,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
 
     constexpr uint32_t id_qk_b = idesc_bf16(64, kChunk, false, false), id_qk_h = idesc_f16(id_qk_b);
-    constexpr uint32_t id_pv_b = idesc_bf16(64, 256, false, true), id_pv_h = idesc_f16(id_pv_b);
+    constexpr uint32_t id_pv = idesc_f16(idesc_bf16(64, 256, false, true));
     auto t_s = [&](int buf) { return tmem + 256u + 64u * (uint32_t)buf; };
 
     if (warp == kWarpQK) {
@@ -522,22 +554,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t ka0 = (uint32_t)sw128_desc(smem_u32(stage_s), 16, 1024);
         for (int c = 0; c < nch; ++c) {
             const int st = c & 1;
-            if (nwl > 0 && c == nwl && !warp_wait(&bars.qconv, 0, status, 604)) break;
             if (c >= 2 && !warp_wait(&bars.sempty[st], (uint32_t)(((c - 2) >> 1) & 1), status, 605)) break;
             const uint32_t ka = ka0 + (uint32_t)((st * kStageBytes) >> 4);
-            const uint32_t id = c < nwl ? id_qk_b : id_qk_h;
             if (!warp_wait(&bars.kfull[st][0], (uint32_t)((c >> 1) & 1), status, 606)) break;
             tc_fence_after();
 #pragma unroll
             for (int s = 0; s < 4 * kHalfBlocks; ++s)
                 mma_ss_if(on, t_s(st), qa + (uint32_t)(((s >> 2) * (kH * 128) + (s & 3) * 32) >> 4),
-                          ka + (uint32_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), hi, id, s ? 1u : 0u);
+                          ka + (uint32_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), hi, id_qk_h, s ? 1u : 0u);
             if (!warp_wait(&bars.kfull[st][1], (uint32_t)((c >> 1) & 1), status, 607)) break;
             tc_fence_after();
 #pragma unroll
             for (int s = 4 * kHalfBlocks; s < 36; ++s)
                 mma_ss_if(on, t_s(st), qa + (uint32_t)(((s >> 2) * (kH * 128) + (s & 3) * 32) >> 4),
-                          ka + (uint32_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), hi, s < 32 ? id : id_qk_b, 1u);
+                          ka + (uint32_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), hi, s < 32 ? id_qk_h : id_qk_b, 1u);
             commit_if(on, &bars.sfull[st]);
         }
     } else if (warp == kWarpPV) {
@@ -552,13 +582,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_fence_after();
             const uint32_t pa = pa0 + (uint32_t)((st * kStageBytes) >> 4);
             const uint32_t va = va0 + (uint32_t)((st * kStageBytes) >> 4);
-            const uint32_t id = c < nwl ? id_pv_b : id_pv_h;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ss_if(on, tmem + (half ? (16u << 16) : 0u), pa + (uint32_t)((kk * 32) >> 4),
-                              va + (uint32_t)((half * kHalfBlocks * kBlk + kk * 2048) >> 4), hi, id, (c | kk) ? 1u : 0u);
+                              va + (uint32_t)((half * kHalfBlocks * kBlk + kk * 2048) >> 4), hi, id_pv, (c | kk) ? 1u : 0u);
                 // dims 0-255 read column blocks 0-3; blocks 4-8 are released after the rest
                 commit_if(on, &bars.kempty[st][half]);
             }
@@ -577,6 +606,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 if (c > 0) load_window(c);   // the first is on its way
                 cp_async_wait<0>();
+                __syncwarp();
+                // content to fp16 in place (a lane's own copies): this warp's rows, 64 chunks each
+#pragma unroll 4
+                for (int i = lane; i < kRowsPerWarp * 64; i += 32) {
+                    uint4* x = reinterpret_cast<uint4*>(dst + ((i & 63) >> 3) * kBlk + sw128_off(pw * kRowsPerWarp + (i >> 6), i & 7));
+                    const uint4 v = *x;
+                    *x = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -595,14 +632,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ok = false;
                     break;
                 }
-                // piece p = (lane >> 3) + 4 i: codes 32 p .. 32 p + 31, 16-byte chunks 4 (p & 1) .. + 3 of column
-                // block p / 2.  A store's eight lanes hold eight rows: eight bank groups.
+                // piece p: codes 32 p .. 32 p + 31, 16-byte chunks 4 (p & 1) .. + 3 of column block p / 2.  A store's
+                // eight lanes differ in the row's low bits or (four rows a warp) in p & 1: eight bank groups.
 #pragma unroll
-                for (int i = 2 * hf; i < 2 * hf + 2; ++i) {
-                    const uint32_t sw = i == 0 ? raw.scales.x : i == 1 ? raw.scales.y : i == 2 ? raw.scales.z : raw.scales.w;
-                    const uint32_t s2 = live ? scale_f16x2(sw, lane >> 3) : 0u;
+                for (int i = hf * (8 / kPieces); i < (hf + 1) * (8 / kPieces); ++i) {
+                    const int p = my_piece + kPieces * i;
+                    const uint32_t sw = p < 8 ? (p < 4 ? raw.scales.x : raw.scales.y) : (p < 12 ? raw.scales.z : raw.scales.w);
+                    const uint32_t s2 = live ? scale_f16x2(sw, p & 3) : 0u;
                     const uint4 cv = live ? raw.codes[i] : make_uint4(0, 0, 0, 0);
-                    const int p = (lane >> 3) + 4 * i;
                     uint8_t* blk = dst + (p >> 1) * kBlk;
                     const int ch = 4 * (p & 1);
                     *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch)) = widen8_cvt(cv.x, s2);
@@ -612,8 +649,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 if (hf) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        *reinterpret_cast<uint4*>(dst + 8 * kBlk + sw128_off(my_row, (lane >> 3) + 4 * i)) =
+                    for (int i = 0; i < 8 / kPieces; ++i)
+                        *reinterpret_cast<uint4*>(dst + 8 * kBlk + sw128_off(my_row, my_piece + kPieces * i)) =
                             live ? raw.rope[i] : make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
@@ -627,50 +664,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (c + 2 < nch) nxt = row_of(c + 2);
         }
         cp_async_wait<0>();
-    } else if (warp < 4) {
-        // ---------------- softmax: warp q owns heads 16q..16q+15; lane l works on head 16q + (l & 15), on
-        // S columns 0-31 (lanes 0-15) or 32-63 (lanes 16-31)
+    } else if (warp < kSoftWarps) {
+        // ---------------- softmax: warp w owns heads 16w .. + 15; lane l works on head 16w + (l & 15), on S columns
+        // 0-31 (lanes 0-15) or 32-63 (lanes 16-31)
         const int head = warp * 16 + (lane & 15);
         const int cbase = (lane < 16) ? 0 : 32;
         float m_used = -INFINITY, l_sum = 0.f;   // log2 domain; weights are 2^(s - m_used + kLift)
-        const float sl2 = nch > 0 ? a.scale * kLog2e * bars.qscale[head] : 0.f;
+        const float sl2 = a.scale * kLog2e * bars.qscale[head];
         const uint32_t flip = sl2 < 0.f ? 0x80000000u : 0u;
         for (int c = 0; c < nch; ++c) {
             const int st = c & 1;
-            const bool wchunk = c < nwl;
             if (!warp_wait(&bars.sfull[st], (uint32_t)((c >> 1) & 1), status, 620)) break;
             tc_fence_after();
-            if (wchunk && c + 1 == nwl && nwl < nch) {
-                // the last window chunk's Q.K^T is done: Q's content to fp16, in place
-                for (int i = threadIdx.x; i < kH * 64; i += 128) {
-                    uint4* p = reinterpret_cast<uint4*>(q_s) + i;
-                    const uint4 v = *p;
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        o[k] = pack_f16x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
-                    *p = make_uint4(o[0], o[1], o[2], o[3]);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&bars.qconv);
-            }
             uint32_t sv[32];
             tmem_ld16x2_32(tmem_addr(t_s(st), warp * 32, 0), sv);
             tmem_ld_wait();
             tc_fence_before();
-            mbar_arrive(&bars.sempty[st]);
-            const int valid = chunk_valid(gcof(c));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.sempty[st]);
             // the maximum of scale * s is that of s (of -s for a negative scale) times |scale|
-            float mx = -INFINITY;
-            if (valid == kChunk) {
+            const int valid = chunk_valid(gcof(c)) - cbase;
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (valid >= 32) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(sv[j] ^ flip));
+                for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(sv[j] ^ flip));
             } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    if (cbase + j < valid) mx = fmaxf(mx, __uint_as_float(sv[j] ^ flip));
+                    if (j < valid) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(sv[j] ^ flip));
             }
+            float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * fabsf(sl2);
             float alpha = 1.f;
             bool rescale = false;
@@ -681,36 +704,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 m_used = m_new;
             }
             const float off = m_used == -INFINITY ? 0.f : m_used - kLift;   // every score -inf: weights 0
+            // p to fp16 and into the RoPE block, 16 bytes at a time
             uint8_t* pblk = stage_s + st * kStageBytes + 8 * kBlk;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) sv[j] = __float_as_uint(ex2(fmaf(__uint_as_float(sv[j]), sl2, -off)));
-            if (valid < kChunk) {   // columns past the chunk's rows weigh nothing
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (cbase + j >= valid) sv[j] = 0u;
-            }
             float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < 32; ++j) ps[j & 3] += __uint_as_float(sv[j]);
-            float psum = (ps[0] + ps[1]) + (ps[2] + ps[3]);
-            if (wchunk) {
+            for (int ch = 0; ch < 4; ++ch) {
+                uint32_t pk[4];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) sv[j] = pack_bf16x2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1]));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) sv[j] = pack_f16x2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1]));
+                for (int q = 0; q < 4; ++q) {
+                    const int j = 8 * ch + 2 * q;
+                    float p0 = ex2(fmaf(__uint_as_float(sv[j]), sl2, -off));
+                    float p1 = ex2(fmaf(__uint_as_float(sv[j + 1]), sl2, -off));
+                    if (j >= valid) p0 = 0.f;   // columns past the chunk's rows weigh nothing
+                    if (j + 1 >= valid) p1 = 0.f;
+                    ps[q] += p0 + p1;
+                    pk[q] = pack_f16x2(p0, p1);
+                }
+                *reinterpret_cast<uint4*>(pblk + sw128_off(head, (cbase >> 3) + ch)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-                *reinterpret_cast<uint4*>(pblk + sw128_off(head, (cbase >> 3) + ch)) =
-                    make_uint4(sv[4 * ch], sv[4 * ch + 1], sv[4 * ch + 2], sv[4 * ch + 3]);
-            psum += __shfl_xor_sync(0xffffffffu, psum, 16);
-            l_sum = l_sum * alpha + psum;
             if (__any_sync(0xffffffffu, rescale)) {
                 // O may be written once the previous chunk's P.V is done
                 if (!warp_wait(&bars.ofull[(c - 1) & 1], (uint32_t)(((c - 1) >> 1) & 1), status, 621)) break;
                 tc_fence_after();
                 const float f = rescale ? alpha : 1.f;
+#pragma unroll 1
                 for (int j = 0; j < 256 / 16; ++j) {
                     uint32_t ov[16];
                     const uint32_t ta = tmem_addr(tmem, warp * 32, j * 16);
@@ -724,21 +741,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_before();
             }
             fence_proxy_async_smem();
-            mbar_arrive(&bars.pfull[st]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.pfull[st]);
+            float psum = (ps[0] + ps[1]) + (ps[2] + ps[3]);
+            psum += __shfl_xor_sync(0xffffffffu, psum, 16);
+            l_sum = l_sum * alpha + psum;
         }
-        // ---- O.  Lane l of warp q holds the O row of head 16q + (l & 15), dims 0-255 (lanes 0-15) or 256-511
+        // ---- O.  Lane l of warp w holds the O row of head 16w + (l & 15), dims 0-255 (lanes 0-15) or 256-511
         // (lanes 16-31).  The only split: normalised, staged through shared memory.  One of several: the
-        // partial and (m, l), for the cluster's merge staged in fp32, else written as the lanes hold it
-        // ([quarter][4 dims][lane], 512 bytes a store).
+        // partial and (m, l) as the lanes hold them ([quarter][4 dims][lane], 512 bytes a store).
         if (nch > 0) warp_wait(&bars.odone, 0, status, 622);
         tc_fence_after();
-        const bool final_out = splits == 1;
-        const float fs = final_out ? ((l_sum > 0.f) ? 1.f / l_sum : 0.f) : 1.f;
+        const bool only = splits == 1;
+        const float fs = only ? ((l_sum > 0.f) ? 1.f / l_sum : 0.f) : 1.f;
         const int dim0 = (lane < 16) ? 0 : 256;
-        const bool f32 = !final_out || a.out_dtype == LCS_F32;
+        const bool f32 = a.out_dtype == LCS_F32;
         uint8_t* rowp = stage_s + head * (f32 ? kOPitchF32 : kOPitchBF16);
         float4* gpart = reinterpret_cast<float4*>(part_o) + ((int64_t)(unit * splits + sp) * 4 + warp) * (64 * 32) + lane;
-        for (int j0 = 0; j0 < 256 / 16; j0 += 4) {
+#pragma unroll 1
+        for (int j0 = 0; j0 < 16; j0 += 4) {
             uint32_t ov[4][16];
             if (nch > 0) {
 #pragma unroll
@@ -753,13 +774,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int j = j0 + u;
-                if (f32) {
+                if (!only || f32) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float4 v =
                             make_float4(__uint_as_float(ov[u][4 * q]) * fs, __uint_as_float(ov[u][4 * q + 1]) * fs,
                                         __uint_as_float(ov[u][4 * q + 2]) * fs, __uint_as_float(ov[u][4 * q + 3]) * fs);
-                        if (final_out || cmerge) reinterpret_cast<float4*>(rowp + (dim0 + j * 16) * 4)[q] = v;
+                        if (only) reinterpret_cast<float4*>(rowp + (dim0 + j * 16) * 4)[q] = v;
                         else __stcg(gpart + (4 * j + q) * 32, v);
                     }
                 } else {
@@ -774,11 +795,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (lane < 16) {
             const float m = l_sum > 0.f ? m_used - kLift : -INFINITY;
-            if (final_out) {
+            if (only) {
                 if (a.lse != nullptr && head < nh)
                     a.lse[(int64_t)g * a.H + h0 + head] = l_sum > 0.f ? (m + log2f(l_sum)) / kLog2e : -INFINITY;
             } else {
-                float* ml = cmerge ? ml_s + 2 * head : part_ml + ((int64_t)(unit * splits + sp) * kH + head) * 2;
+                float* ml = part_ml + ((int64_t)(unit * splits + sp) * kH + head) * 2;
                 ml[0] = m;
                 ml[1] = l_sum;
             }
@@ -787,64 +808,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (cmerge) {
-        // ---- split merge inside the cluster: split sp merges heads sp, sp + splits, ... from every
-        // split's staged O and (m, l) over distributed shared memory, in split order
-        cluster_sync_all();
-        constexpr int kW = kMaxCluster + 2;
-        float* wt = ml_s + 2 * kH;   // [heads of this split][f_0 .. f_{splits-1}, 1/L]
-        const int nm = sp < nh ? (nh - sp + splits - 1) / splits : 0;
-        if ((int)threadIdx.x < nm) {
-            const int h = sp + (int)threadIdx.x * splits;
-            float M = -INFINITY;
-            for (int r = 0; r < splits; ++r) {
-                const float m = ld_dsmem_f32(dsmem_addr(ml_s + 2 * h, (uint32_t)r));
-                const float l = ld_dsmem_f32(dsmem_addr(ml_s + 2 * h + 1, (uint32_t)r));
-                if (l > 0.f) M = fmaxf(M, m);
-            }
-            float Ls = 0.f;
-            for (int r = 0; r < splits; ++r) {
-                const float m = ld_dsmem_f32(dsmem_addr(ml_s + 2 * h, (uint32_t)r));
-                const float l = ld_dsmem_f32(dsmem_addr(ml_s + 2 * h + 1, (uint32_t)r));
-                const float f = l > 0.f ? exp2f(m - M) : 0.f;
-                wt[threadIdx.x * kW + r] = f;
-                Ls += l * f;
-            }
-            wt[threadIdx.x * kW + kMaxCluster] = Ls > 0.f ? 1.f / Ls : 0.f;
-            if (a.lse != nullptr) a.lse[(int64_t)g * a.H + h0 + h] = Ls > 0.f ? (M + log2f(Ls)) / kLog2e : -INFINITY;
-        }
-        __syncthreads();
-        for (int it = (int)threadIdx.x; it < nm * (kDv / 4); it += kTcThreads) {
-            const int i = it / (kDv / 4), q4 = it - i * (kDv / 4);
-            const int h = sp + i * splits;
-            const float* rw = wt + i * kW;
-            const uint8_t* src = stage_s + h * kOPitchF32 + q4 * 16;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int r = 0; r < splits; ++r) {
-                const float4 v = ld_dsmem_f4(dsmem_addr(src, (uint32_t)r));
-                const float f = rw[r];
-                acc.x += v.x * f;
-                acc.y += v.y * f;
-                acc.z += v.z * f;
-                acc.w += v.w * f;
-            }
-            const float iv = rw[kMaxCluster];
-            const int64_t o4 = ((int64_t)g * a.H + h0 + h) * (kDv / 4) + q4;
-            if (a.out_dtype == LCS_F32)
-                reinterpret_cast<float4*>(a.out)[o4] = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
-            else
-                reinterpret_cast<uint2*>(a.out)[o4] =
-                    make_uint2(pack_bf16x2(acc.x * iv, acc.y * iv), pack_bf16x2(acc.z * iv, acc.w * iv));
-        }
-        cluster_sync_all();   // no CTA leaves while a peer still reads its staged partial
-    } else if (splits == 1) {
+    if (splits == 1) {
         // the staged output rows with coalesced 16-byte stores
         const bool f32 = a.out_dtype == LCS_F32;
         const int pitch = f32 ? kOPitchF32 : kOPitchBF16;
         const int rb = f32 ? kDv * 4 : kDv * 2;
         uint8_t* gout = static_cast<uint8_t*>(a.out) + ((int64_t)g * a.H + h0) * rb;
+#pragma unroll 2
         for (int off = (int)threadIdx.x * 16; off < nh * rb; off += kTcThreads * 16) {
-            const int h = off / rb, cb = off - h * rb;
+            const int h = f32 ? off >> 11 : off >> 10, cb = off & (rb - 1);
             *reinterpret_cast<uint4*>(gout + off) = *reinterpret_cast<const uint4*>(stage_s + h * pitch + cb);
         }
     }
@@ -876,6 +848,13 @@ __global__ void __launch_bounds__(kMergeThreads)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 #endif
     if (h0 >= H) return;
+    const float4* src = reinterpret_cast<const float4*>(part_o) +
+                        (((int64_t)unit * splits * 4 + quarter) * 64 + 8 * part + warp) * 32 + lane;
+    constexpr int kFly = 8;
+    float4 v[kFly];
+#pragma unroll
+    for (int k = 0; k < kFly; ++k)
+        if (k < splits) v[k] = __ldcg(src + (int64_t)k * (4 * 64 * 32));
     for (int i = 2 * warp; i < 2 * warp + 2; ++i) {
         float2 ml[2];
         float M = -INFINITY;
@@ -903,17 +882,11 @@ __global__ void __launch_bounds__(kMergeThreads)
         }
     }
     __syncthreads();
-    const float4* src = reinterpret_cast<const float4*>(part_o) +
-                        (((int64_t)unit * splits * 4 + quarter) * 64 + 8 * part + warp) * 32 + lane;
     const int i = lane & 15;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < splits; s0 += 8) {
-        float4 v[8];
+    for (int s0 = 0; s0 < splits; s0 += kFly) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (s0 + k < splits) v[k] = __ldcg(src + (int64_t)(s0 + k) * (4 * 64 * 32));
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < kFly; ++k)
             if (s0 + k < splits) {
                 const float e = fac[i][s0 + k];
                 acc.x += v[k].x * e;
@@ -921,6 +894,9 @@ __global__ void __launch_bounds__(kMergeThreads)
                 acc.z += v[k].z * e;
                 acc.w += v[k].w * e;
             }
+#pragma unroll
+        for (int k = 0; k < kFly; ++k)
+            if (s0 + kFly + k < splits) v[k] = __ldcg(src + (int64_t)(s0 + kFly + k) * (4 * 64 * 32));
     }
     const float iv = inv_l[i];
     o_s[lane][4 * warp] = acc.x * iv;
@@ -928,6 +904,10 @@ __global__ void __launch_bounds__(kMergeThreads)
     o_s[lane][4 * warp + 2] = acc.z * iv;
     o_s[lane][4 * warp + 3] = acc.w * iv;
     __syncthreads();
+#if defined(__CUDA_ARCH__)
+    // the partials are read: the next kernel of the stream may be set up
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+#endif
     // row r of o_s: head r & 15, dims (r < 16 ? 0 : 256) + 32 part + column
     const int r = t >> 3, c4 = (t & 7) * 4;
     if (h0 + (r & 15) < H) {
@@ -961,36 +941,6 @@ int kv4_splits(const AttendKv4Args& a) {
     return best;
 }
 
-// Whether all of the launch's clusters of `splits` CTAs can be resident at once (asked once per
-// device and split count).
-bool kv4_cluster_ok(int splits, int64_t units) {
-    if (splits < 2 || splits > kMaxCluster) return false;
-    constexpr int kDevices = 16;
-    static std::mutex mu;
-    static int cache[kDevices][kMaxCluster + 1];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return false;
-    std::lock_guard<std::mutex> lock(mu);
-    if (cache[dev][splits] == 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)splits);
-        cfg.blockDim = dim3(kTcThreads);
-        cfg.dynamicSmemBytes = kTcSmem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)splits;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, attend_kv4_tc_kernel, &cfg) != cudaSuccess) n = 0;
-        cudaGetLastError();
-        cache[dev][splits] = n > 0 ? n : -1;
-    }
-    return cache[dev][splits] >= units;
-}
-
 cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaStream_t s) {
     const int tiles = (a.H + kH - 1) / kH;
     const int64_t units = a.B * a.Q * tiles;
@@ -1003,21 +953,9 @@ cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaSt
         part_o = static_cast<float*>(scratch);
         part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + align256(units * splits * kH * kDv * 4));
     }
-    const int cmerge = kv4_cluster_ok(splits, units) ? 1 : 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = splits > 1 ? dim3((unsigned)splits, (unsigned)units) : dim3((unsigned)units);
-    cfg.blockDim = dim3(kTcThreads);
-    cfg.dynamicSmemBytes = kTcSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cmerge;
-    e = cudaLaunchKernelEx(&cfg, attend_kv4_tc_kernel, a, tiles, splits, cmerge, part_o, part_ml, status);
-    if (e != cudaSuccess || splits == 1 || cmerge) return e;
+    e = launch_k(attend_kv4_tc_kernel, splits > 1 ? dim3((unsigned)splits, (unsigned)units) : dim3((unsigned)units),
+                 dim3(kTcThreads), kTcSmem, s, true, a, tiles, splits, part_o, part_ml, status);
+    if (e != cudaSuccess || splits == 1) return e;
     return launch_k(kv4_merge_kernel, dim3((unsigned)(units * 32)), dim3(kMergeThreads), 0, s, true, part_o, part_ml,
                     splits, a.H, tiles, a.out, a.out_dtype, a.lse);
 }
