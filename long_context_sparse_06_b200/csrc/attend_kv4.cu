@@ -191,66 +191,78 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
 }
 
 // ----------------------------------------------------------- tensor-core path
-// bf16 queries, d_c = 512, d_r = 64.  One CTA (448 threads) per (query, tile of 64 heads, split of
-// its row list); the row list is the window rows, padded to whole chunks of 64, then the selected
-// or available entries; chunk i goes to split i mod splits.
+// bf16 queries, d_c = 512, d_r = 64.  One CTA (18 warps) per (query, tile of 64 heads, split of its
+// row list); the row list is the window rows, padded to whole chunks of 48, then the selected or
+// available entries; chunk i goes to split i mod splits.
 //
-//   S [64 heads x 64 rows] = Q [64 x 576] . K_chunk^T,  O [64 x 512] += P [64 x 64] . V_chunk
+//   S [64 heads x 48 rows] = Q [64 x 576] . K_chunk^T,  O [64 x 512] += P [64 x 48] . V_chunk
 //
-// on tcgen05.mma with the heads as M = 64 (fp32 accumulators in TMEM: O as two interleaved M = 64
-// accumulators in columns 0-255, S double-buffered in 256-383).
+// on tcgen05.mma with the heads as M = 64, fp32 accumulators in TMEM.
 //
 //  * Widening.  code x scale has at most six significant bits and lies in [2^-10, 2688], so it is
 //    exact in fp16: one conversion per pair of codes and one fp16 multiply by the scale, half of what
-//    bf16 would take.  Both operands of a kind::f16 MMA have one type, so for these chunks the
-//    content dims of Q are fp16 too, scaled per head by a power of two that puts the head's largest
-//    element in [2^14, 2^15) (exact down to 2^-28 of it, below that off by 2^-39 of it), and P is fp16
-//    (11 bits; 2^-11 a weight, against 2^-8 of bf16).  RoPE dims stay bf16: four MMAs of the same
+//    bf16 would take.  Both operands of a kind::f16 MMA have one type, so the content dims of Q are
+//    fp16 too, scaled per head by a power of two that puts the head's largest element in
+//    [2^14, 2^15) (exact down to 2^-28 of it, below that off by 2^-39 of it), and P is fp16 (11
+//    bits; 2^-11 a weight, against 2^-8 of bf16).  RoPE dims stay bf16: four MMAs of the same
 //    accumulation.  Window rows' content goes from bf16 to fp16 as well: exact from 2^-14 to 65504
 //    (their bf16 has 8 bits), off by 2^-25 below, where 4-bit rows resolve 2^-10, and saturating
 //    above, where 4-bit rows end at 2688.
-//  * A chunk's 64 widened rows (72 KB) are the K-major B of Q.K^T and the MN-major B of P.V;
-//    two stages, each released in two halves of the columns as P.V leaves them.  Warps 4-11
-//    fill: a warp owns 8 rows and holds the next chunk's 400-byte rows in registers (six 16-byte loads
-//    a lane) while it waits for its stage; eight lanes take one row's 128 bytes of codes, each
-//    writing its four 16-byte results in a rotated order so that a store's eight lanes
-//    meet eight different bank groups.
-//  * Warps 12 and 13 issue the MMAs with the whole warp in step and an elected lane's predicate on
+//  * Shared memory is what an SM runs out of: its bandwidth (an MMA with both operands in it takes
+//    4 KB per 32 cycles) and its size (a chunk is the K-major B of Q.K^T and the MN-major B of P.V).
+//    So P and 320 of Q's dims are A operands in TMEM, in the lanes of the accumulator they
+//    meet: S of even and odd chunks and O's dims 0-255 and 256-511 use the two halves of every 32
+//    lanes, and Q and P are kept in both.  That leaves room for three stages of 48 rows, each
+//    released in two halves of the columns as P.V leaves them: widening, Q.K^T, softmax and P.V of
+//    different chunks run side by side (two stages of 64 rows took 3400 cycles per 64 rows, where
+//    each step was the others' wait).
+//  * Warps 4-9 fill the even chunks, warps 10-15 the odd ones: a warp owns 8 rows and holds its next
+//    chunk's 400-byte rows in registers (seven 16-byte loads a lane), which then have two chunks'
+//    time to arrive (one group alone waited 1500 cycles for them, chunk after chunk).
+//  * Warps 16 and 17 issue the MMAs with the whole warp in step and an elected lane's predicate on
 //    the instruction: 35 cycles per M = 64, N = 64 MMA alone on the SM (32 is its rate), where
-//    issue from a branch of one thread took 55 to 72 and was what a chunk waited for.
-//  * Warps 0-3 run the online softmax (fp32, exp2).  Weights are kept 2^6 above 1, so that
-//    fp16 reaches down to 2^-31 of the largest; O is rescaled when a head's maximum grows by more
-//    than 2^8.
-//  * P lies in the chunk's RoPE column block, which is dead once Q.K^T has read it.
-constexpr int kH = 64, kD = 576, kDv = 512, kChunk = 64;
-constexpr int kBlk = kChunk * 128;            // one SW128 column block of a chunk: 64 rows x 128 B
-constexpr int kStageBytes = 9 * kBlk;         // 72 KB
-constexpr int kQBytes = 9 * (kH * 128);       // 72 KB
-constexpr int kSoftWarps = 4, kProdWarps = 8;
-constexpr int kWarpQK = kSoftWarps + kProdWarps, kWarpPV = kWarpQK + 1, kTcWarps = kWarpPV + 1;
+//    issue from a branch of one thread took 55 to 72.
+//  * Warps 0-3 bring in Q and run the online softmax (fp32, exp2).  Weights are kept 2^6 above 1, so
+//    that fp16 reaches down to 2^-31 of the largest; O is rescaled when a head's maximum grows by
+//    more than 2^8.
+constexpr int kH = 64, kD = 576, kDv = 512, kChunk = 48, kStages = 3;
+constexpr int kBlk = kChunk * 128;            // one SW128 column block of a chunk: 48 rows x 128 B
+constexpr int kStageBytes = 9 * kBlk;         // 54 KB
+constexpr int kQBlk = kH * 128;               // one SW128 column block of Q
+constexpr int kTQ = 320;                      // Q's dims 0 .. kTQ-1 in TMEM, the others in shared memory
+constexpr int kQBytes = (9 - kTQ / 64) * kQBlk;
+constexpr int kSoftWarps = 4, kProdWarps = 6, kProdGroups = 2;
+constexpr int kWarpQK = kSoftWarps + kProdGroups * kProdWarps, kWarpPV = kWarpQK + 1, kTcWarps = kWarpPV + 1;
 constexpr int kTcThreads = kTcWarps * 32;
 constexpr int kRowsPerWarp = kChunk / kProdWarps;             // rows of a chunk per producer warp
 constexpr int kPieces = 32 / kRowsPerWarp;                    // lanes that share a row
-static_assert(kRowsPerWarp == 4 || kRowsPerWarp == 8, "a store's eight lanes meet eight bank groups");
+static_assert(kRowsPerWarp == 8, "a store's eight lanes hold eight rows: eight bank groups");
 constexpr int kHalfBlocks = 4;                // column blocks of a stage's first half
-constexpr size_t kTcSmem = 1024 + kQBytes + 2 * kStageBytes;
+constexpr size_t kTcSmem = 1024 + kQBytes + kStages * kStageBytes;
 constexpr int kMaxSplits = 64;
 constexpr int kOPitchF32 = kDv * 4 + 16;      // staged O rows (padded)
 constexpr int kOPitchBF16 = kDv * 2 + 16;
-static_assert(kH * kOPitchF32 <= 2 * kStageBytes, "staged O fits in the stages");
+static_assert(kH * kOPitchF32 <= kStages * kStageBytes, "staged O fits in the stages");
+static_assert(kTQ / 64 * kQBlk <= kStageBytes, "Q's TMEM part passes through the last stage");
+// TMEM columns: O, S (even chunks in lanes 0-15 of each 32, odd ones in lanes 16-31), P of even and
+// of odd chunks, Q (the last three twice, for both halves of the lanes).
+constexpr uint32_t kTmS = 256, kTmP = kTmS + kChunk, kTmQ = kTmP + 2 * (kChunk / 2), kHi16 = 16u << 16;
+static_assert(kTmQ + kTQ / 2 <= 512, "TMEM columns");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.0f;              // log2 of the tolerated growth before O is rescaled
 constexpr float kLift = 6.0f;                 // log2 of the largest weight when the maximum is current
 
 struct TcBars {
-    uint64_t kfull[2][2], kempty[2][2];       // [stage][half]
-    uint64_t sfull[2], sempty[2];
+    uint64_t kfull[kStages][2], kempty[kStages][2];   // [stage][half]
+    uint64_t sfull[2], sempty[2];             // per chunk parity, like the next two
     uint64_t pfull[2];
-    uint64_t ofull[2];                        // P.V of chunk c done (per chunk parity)
+    uint64_t ofull[2];                        // P.V of the chunk done
     uint64_t odone;                           // every P.V of this CTA done
+    uint64_t qfull;                           // Q is where the MMAs read it
     uint32_t tmem_base;
     int first_bad[kTcWarps];
     float qscale[kH];                         // 2^-e of head h: the true q is the stored one times it
+    float inv_l[kH];
 };
 
 // One lane of the (converged) warp, the same at every call.
@@ -273,6 +285,18 @@ __device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint32_t a, u
         "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(on), "r"(hi)
         : "memory");
 }
+// The same with A in TMEM (fp16 pairs, row i in the lane of the accumulator's row i).
+__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t hi,
+                                          uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "mov.b64 db, {%2, %6};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b), "r"(idesc), "r"(acc), "r"(on), "r"(hi)
+        : "memory");
+}
 // The elected lane's commit: arrives once on `bar` when its MMAs so far are complete.
 __device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
     asm volatile(
@@ -286,8 +310,8 @@ __device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t bf16) { return bf16 & ~((1u << 7) | (1u << 10)); }
 
 // A bounded wait that the whole warp leaves with one answer.  The thread sleeps in the hardware's wait
-// (up to the hint, 20 us) instead of polling: two dozen polling warps took the issue slots of the
-// few that had work.  The clock and the grid's status word are looked at after every 16 sleeps.
+// (up to the hint, 20 us) instead of polling.  The clock and the grid's status word are looked at
+// after every 16 sleeps.
 __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -315,6 +339,17 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* s
 __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The larger magnitude of either half (its sign is that of the product's).
+__device__ __forceinline__ uint32_t bf16x2_maxabs(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -358,6 +393,25 @@ __device__ __forceinline__ uint4 widen8_perm(uint32_t w, uint32_t s2) {
     return make_uint4(f16x2_mul(__byte_perm(r0, 0, 0x1404), s2), f16x2_mul(__byte_perm(r0, 0, 0x3424), s2),
                       f16x2_mul(__byte_perm(r1, 0, 0x1404), s2), f16x2_mul(__byte_perm(r1, 0, 0x3424), s2));
 }
+// 16 lanes x 32 bits, two column ranges 24 apart: threads 0-15 read lanes base..base+15 at columns
+// [c, c+n), threads 16-31 the same lanes at columns [c+24, c+24+n).
+__device__ __forceinline__ void tmem_ld16x2_8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 24;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16x2_16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 24;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 // The E4M3 scale in byte `at` of w, as fp16 in both halves.
 __device__ __forceinline__ uint32_t scale_f16x2(uint32_t w, int at) {
     uint32_t r;
@@ -393,20 +447,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int nh = min(kH, a.H - h0);
     const int b = a.Q == 1 ? g : (int)((unsigned)g / (unsigned)a.Q);
     const bool producer = warp >= kSoftWarps && warp < kWarpQK;
-    const int pw = warp - kSoftWarps;
+    const int pg = warp >= kSoftWarps + kProdWarps ? 1 : 0;   // a producer's group, and its place there
+    const int pw = warp - kSoftWarps - pg * kProdWarps;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kStages; ++i)
             for (int hf = 0; hf < 2; ++hf) {
                 mbar_init(&bars.kfull[i][hf], kProdWarps);
                 mbar_init(&bars.kempty[i][hf], 1);
             }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.pfull[i], kSoftWarps);
             mbar_init(&bars.sfull[i], 1);
             mbar_init(&bars.sempty[i], kSoftWarps);
             mbar_init(&bars.ofull[i], 1);
         }
         mbar_init(&bars.odone, 1);
+        mbar_init(&bars.qfull, kSoftWarps);
         fence_barrier_init();
     }
     if (warp == kWarpQK) {
@@ -416,14 +473,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #if defined(__CUDA_ARCH__)
     asm volatile("griddepcontrol.wait;" ::: "memory");   // everything above reads no memory of the call
 #endif
-    // ---- the loads that nothing waits for, before everything else: Q as it is, in the SW128 layout (16-byte
-    // chunk c of head h: column block c / 8) ...
+    // column block k of Q: the first ones pass through the last stage into TMEM
+    auto q_block = [&](int k) { return k < kTQ / 64 ? stage_s + (kStages - 1) * kStageBytes + k * kQBlk : q_s + (k - kTQ / 64) * kQBlk; };
+    // ---- the loads that nothing waits for, before everything else: Q as it is, in the SW128 layout ...
     {
         const uint8_t* qg = static_cast<const uint8_t*>(a.q) + ((int64_t)g * a.H + h0) * (kD * 2);
-#pragma unroll 1
+#pragma unroll 4
         for (int i = threadIdx.x; i < kH * 72; i += kTcThreads) {
             const int h = i / 72, c = i - h * 72;
-            cp_async_16(q_s + (c >> 3) * (kH * 128) + sw128_off(h, c & 7), qg + (h < nh ? i * 16 : 0), h < nh);
+            cp_async_16(q_block(c >> 3) + sw128_off(h, c & 7), qg + (h < nh ? i * 16 : 0), h < nh);
         }
         cp_async_commit();
     }
@@ -454,9 +512,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             raw.scales = __ldg(reinterpret_cast<const uint4*>(src) + 24);
         }
     };
-    // window chunk c of this split into stage c & 1: bf16 rows by 16-byte cp.async, zeros past the last row
-    auto load_window = [&](int c) {
-        uint8_t* dst = stage_s + (c & 1) * kStageBytes;
+    // window chunk c of this split into its stage st: bf16 rows by 16-byte cp.async, zeros past the last row
+    auto load_window = [&](int c, int st) {
+        uint8_t* dst = stage_s + st * kStageBytes;
         const int64_t w0 = (int64_t)gcof(c) * kChunk;
         const uint8_t* src = static_cast<const uint8_t*>(a.win) + ((int64_t)b * a.Tw + wp.lo + w0) * (kD * 2);
 #pragma unroll 1
@@ -468,14 +526,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         cp_async_commit();
     };
+    // a group's first compressed chunk, the next one it takes being two on
+    const int first = nwl + ((nwl ^ pg) & 1);
     const uint8_t *cur = nullptr, *nxt = nullptr;
     if (producer) {
-        cur = row_of(nwl);
+        cur = row_of(first);
         load_row(cur);
-        if (nwl > 0) load_window(0);
-        nxt = row_of(nwl + 1);
+        if (pg < nwl) load_window(pg, pg);
+        nxt = row_of(first + 2);
     }
-
     // ---- selection length (CSA: the valid prefix of idx): a minimum per warp, joined below
     if (sel != nullptr) {
         int first_bad = a.k;
@@ -491,38 +550,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---- Q scaled by 2^e in place, a warp per head; content to fp16
 #pragma unroll 1
     for (int h = warp; h < kH; h += kTcWarps) {
-        uint8_t* qh = q_s + (lane >> 3) * (kH * 128) + sw128_off(h, lane & 7);   // chunks lane, lane + 32, lane + 64
-        uint4 v[3];
-        v[0] = *reinterpret_cast<const uint4*>(qh);
-        v[1] = *reinterpret_cast<const uint4*>(qh + 4 * (kH * 128));
-        v[2] = make_uint4(0, 0, 0, 0);
-        if (lane < 8) v[2] = *reinterpret_cast<const uint4*>(qh + 8 * (kH * 128));
-        uint32_t mag2 = 0;   // largest magnitudes of the even and odd elements, as bf16 bits
-#pragma unroll
-        for (int c = 0; c < 3; ++c) {
-            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mag2 = __vmaxu2(mag2, w[k] & 0x7FFF7FFFu);
-        }
-        const uint32_t mag = __reduce_max_sync(0xffffffffu, max(mag2 & 0xFFFFu, mag2 >> 16));
+        const uint32_t at = sw128_off(h, lane & 7);   // chunks lane, lane + 32, lane + 64
+        uint4* x0 = reinterpret_cast<uint4*>(q_block(lane >> 3) + at);
+        uint4* x1 = reinterpret_cast<uint4*>(q_block(4 + (lane >> 3)) + at);
+        uint4* x2 = reinterpret_cast<uint4*>(q_block(8) + at);
+        const uint4 v0 = *x0, v1 = *x1, v2 = *x2;     // (four lanes read each of the last 8 chunks)
+        uint32_t m2 = bf16x2_maxabs(bf16x2_maxabs(v0.x, v0.y), bf16x2_maxabs(v0.z, v0.w));
+        m2 = bf16x2_maxabs(m2, bf16x2_maxabs(bf16x2_maxabs(v1.x, v1.y), bf16x2_maxabs(v1.z, v1.w)));
+        m2 = bf16x2_maxabs(m2, bf16x2_maxabs(bf16x2_maxabs(v2.x, v2.y), bf16x2_maxabs(v2.z, v2.w)));
+        const uint32_t mag = __reduce_max_sync(0xffffffffu, max(m2 & 0x7FFFu, (m2 >> 16) & 0x7FFFu));   // bf16 bits
         const int ex = (int)(mag >> 7) - 127;               // of the largest element (subnormals: -127)
         int e = mag == 0 || mag >= 0x7F80u ? 0 : 14 - ex;   // zero, infinite or NaN heads stay as they are
         e = e > 126 ? 126 : e;
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        const uint32_t up2 = (uint32_t)(127 + e) * 0x00800080u;
         if (lane == 0) bars.qscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
-        auto scaled = [&](uint4 x, bool half) {
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float f0 = __uint_as_float(w[k] << 16) * up, f1 = __uint_as_float(w[k] & 0xFFFF0000u) * up;
-                o[k] = half ? pack_f16x2(f0, f1) : pack_bf16x2(f0, f1);
-            }
-            return make_uint4(o[0], o[1], o[2], o[3]);
-        };
-        *reinterpret_cast<uint4*>(qh) = scaled(v[0], true);
-        *reinterpret_cast<uint4*>(qh + 4 * (kH * 128)) = scaled(v[1], true);
-        if (lane < 8) *reinterpret_cast<uint4*>(qh + 8 * (kH * 128)) = scaled(v[2], false);
+        *x0 = make_uint4(bf16x2_to_f16x2(bf16x2_mul(v0.x, up2)), bf16x2_to_f16x2(bf16x2_mul(v0.y, up2)),
+                         bf16x2_to_f16x2(bf16x2_mul(v0.z, up2)), bf16x2_to_f16x2(bf16x2_mul(v0.w, up2)));
+        *x1 = make_uint4(bf16x2_to_f16x2(bf16x2_mul(v1.x, up2)), bf16x2_to_f16x2(bf16x2_mul(v1.y, up2)),
+                         bf16x2_to_f16x2(bf16x2_mul(v1.z, up2)), bf16x2_to_f16x2(bf16x2_mul(v1.w, up2)));
+        if (lane < 8)
+            *x2 = make_uint4(bf16x2_mul(v2.x, up2), bf16x2_mul(v2.y, up2), bf16x2_mul(v2.z, up2), bf16x2_mul(v2.w, up2));
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -541,70 +588,82 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int64_t v = gc < nwc ? wp.n - (int64_t)gc * kChunk : (int64_t)nsel - (int64_t)(gc - nwc) * kChunk;
         return (int)(v < kChunk ? v : kChunk);
     };
-
-    constexpr uint32_t id_qk_b = idesc_bf16(64, kChunk, false, false), id_qk_h = idesc_f16(id_qk_b);
-    constexpr uint32_t id_pv = idesc_f16(idesc_bf16(64, 256, false, true));
-    auto t_s = [&](int buf) { return tmem + 256u + 64u * (uint32_t)buf; };
+    const bool only = splits == 1;
 
     if (warp == kWarpQK) {
         // ---------------- Q.K^T issue
         const uint32_t on = elect_lane();
+        constexpr uint32_t id_b = idesc_bf16(64, kChunk, false, false), id_h = idesc_f16(id_b);
         const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024);
         const uint32_t qa = (uint32_t)q_desc, hi = (uint32_t)(q_desc >> 32);
         const uint32_t ka0 = (uint32_t)sw128_desc(smem_u32(stage_s), 16, 1024);
-        for (int c = 0; c < nch; ++c) {
-            const int st = c & 1;
-            if (c >= 2 && !warp_wait(&bars.sempty[st], (uint32_t)(((c - 2) >> 1) & 1), status, 605)) break;
-            const uint32_t ka = ka0 + (uint32_t)((st * kStageBytes) >> 4);
-            if (!warp_wait(&bars.kfull[st][0], (uint32_t)((c >> 1) & 1), status, 606)) break;
+        int st = 0;
+        uint32_t ph = 0;
+        if (nch > 0 && warp_wait(&bars.qfull, 0, status, 604)) {
             tc_fence_after();
+            for (int c = 0; c < nch; ++c) {
+                const uint32_t half = c & 1 ? kHi16 : 0u;
+                if (c >= 2 && !warp_wait(&bars.sempty[c & 1], (uint32_t)(((c - 2) >> 1) & 1), status, 605)) break;
+                const uint32_t ka = ka0 + (uint32_t)((st * kStageBytes) >> 4);
+                const uint32_t d = tmem + kTmS + half, qt = tmem + kTmQ + half;
+                auto issue = [&](int s0, int s1) {
 #pragma unroll
-            for (int s = 0; s < 4 * kHalfBlocks; ++s)
-                mma_ss_if(on, t_s(st), qa + (uint32_t)(((s >> 2) * (kH * 128) + (s & 3) * 32) >> 4),
-                          ka + (uint32_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), hi, id_qk_h, s ? 1u : 0u);
-            if (!warp_wait(&bars.kfull[st][1], (uint32_t)((c >> 1) & 1), status, 607)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int s = 4 * kHalfBlocks; s < 36; ++s)
-                mma_ss_if(on, t_s(st), qa + (uint32_t)(((s >> 2) * (kH * 128) + (s & 3) * 32) >> 4),
-                          ka + (uint32_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4), hi, s < 32 ? id_qk_h : id_qk_b, 1u);
-            commit_if(on, &bars.sfull[st]);
+                    for (int s = s0; s < s1; ++s) {
+                        const uint32_t kb = ka + (uint32_t)(((s >> 2) * kBlk + (s & 3) * 32) >> 4);
+                        if (s < kTQ / 16) mma_ts_if(on, d, qt + 8 * s, kb, hi, id_h, s ? 1u : 0u);
+                        else
+                            mma_ss_if(on, d, qa + (uint32_t)((((s >> 2) - kTQ / 64) * kQBlk + (s & 3) * 32) >> 4), kb, hi,
+                                      s < 32 ? id_h : id_b, 1u);
+                    }
+                };
+                if (!warp_wait(&bars.kfull[st][0], ph, status, 606)) break;
+                tc_fence_after();
+                issue(0, 4 * kHalfBlocks);
+                if (!warp_wait(&bars.kfull[st][1], ph, status, 607)) break;
+                tc_fence_after();
+                issue(4 * kHalfBlocks, 36);
+                commit_if(on, &bars.sfull[c & 1]);
+                if (++st == kStages) st = 0, ph ^= 1;
+            }
         }
     } else if (warp == kWarpPV) {
         // ---------------- P.V issue (its own warp: it never waits behind the next Q.K^T's rows)
         const uint32_t on = elect_lane();
-        const uint64_t p_desc = sw128_desc(smem_u32(stage_s) + 8 * kBlk, 16, 1024);
-        const uint32_t pa0 = (uint32_t)p_desc, hi = (uint32_t)(p_desc >> 32);
-        const uint32_t va0 = (uint32_t)sw128_desc(smem_u32(stage_s), kBlk, 1024);
+        constexpr uint32_t id = idesc_f16(idesc_bf16(64, 256, false, true));
+        const uint64_t v_desc = sw128_desc(smem_u32(stage_s), kBlk, 1024);
+        const uint32_t va0 = (uint32_t)v_desc, hi = (uint32_t)(v_desc >> 32);
+        int st = 0;
         for (int c = 0; c < nch; ++c) {
-            const int st = c & 1;
-            if (!warp_wait(&bars.pfull[st], (uint32_t)((c >> 1) & 1), status, 608)) break;
+            if (!warp_wait(&bars.pfull[c & 1], (uint32_t)((c >> 1) & 1), status, 608)) break;
             tc_fence_after();
-            const uint32_t pa = pa0 + (uint32_t)((st * kStageBytes) >> 4);
             const uint32_t va = va0 + (uint32_t)((st * kStageBytes) >> 4);
+            const uint32_t pt = tmem + kTmP + (uint32_t)(c & 1) * (kChunk / 2);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ss_if(on, tmem + (half ? (16u << 16) : 0u), pa + (uint32_t)((kk * 32) >> 4),
-                              va + (uint32_t)((half * kHalfBlocks * kBlk + kk * 2048) >> 4), hi, id_pv, (c | kk) ? 1u : 0u);
+                for (int kk = 0; kk < kChunk / 16; ++kk)
+                    mma_ts_if(on, tmem + (half ? kHi16 : 0u), pt + (half ? kHi16 : 0u) + 8 * kk,
+                              va + (uint32_t)((half * kHalfBlocks * kBlk + kk * 2048) >> 4), hi, id, (c | kk) ? 1u : 0u);
                 // dims 0-255 read column blocks 0-3; blocks 4-8 are released after the rest
                 commit_if(on, &bars.kempty[st][half]);
             }
-            commit_if(on, &bars.ofull[st]);
+            commit_if(on, &bars.ofull[c & 1]);
+            if (++st == kStages) st = 0;
         }
         if (nch > 0) commit_if(on, &bars.odone);
     } else if (producer) {
-        // ---------------- producers: this split's chunks in order, stage c & 1
-        for (int c = 0; c < nch; ++c) {
-            const int st = c & 1;
+        // ---------------- producers: this group's chunks in order
+        int st = pg;
+        uint32_t ph = 1;   // of the stage's last release
+        for (int c = pg; c < nch; c += kProdGroups) {
             uint8_t* dst = stage_s + st * kStageBytes;
-            const uint32_t par = (uint32_t)((((c >> 1) - 1)) & 1);
+            // Q's TMEM part leaves the last stage before its first rows come in
+            if (c == kStages - 1 && !warp_wait(&bars.qfull, 0, status, 613)) break;
             if (c < nwl) {
-                if (c >= 2 && (!warp_wait(&bars.kempty[st][0], par, status, 609) ||
-                               !warp_wait(&bars.kempty[st][1], par, status, 610)))
+                if (c >= kStages && (!warp_wait(&bars.kempty[st][0], ph, status, 609) ||
+                                     !warp_wait(&bars.kempty[st][1], ph, status, 610)))
                     break;
-                if (c > 0) load_window(c);   // the first is on its way
+                if (c != pg) load_window(c, st);   // the first is on its way
                 cp_async_wait<0>();
                 __syncwarp();
                 // content to fp16 in place (a lane's own copies): this warp's rows, 64 chunks each
@@ -620,77 +679,96 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     mbar_arrive(&bars.kfull[st][0]);
                     mbar_arrive(&bars.kfull[st][1]);
                 }
-                continue;
+            } else {
+                const bool attended = my_row < chunk_valid(gcof(c));
+                if (attended && cur == nullptr) set_status(status, LCS_ERR_DEVICE, 602);
+                const bool live = attended && cur != nullptr;
+                bool ok = true;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    if (c >= kStages && !warp_wait(&bars.kempty[st][hf], ph, status, 611 + hf)) {
+                        ok = false;
+                        break;
+                    }
+                    // piece p: codes 32 p .. 32 p + 31, 16-byte chunks 4 (p & 1) .. + 3 of column block p / 2
+#pragma unroll
+                    for (int i = hf * (8 / kPieces); i < (hf + 1) * (8 / kPieces); ++i) {
+                        const int p = my_piece + kPieces * i;
+                        const uint32_t sw = p < 8 ? (p < 4 ? raw.scales.x : raw.scales.y) : (p < 12 ? raw.scales.z : raw.scales.w);
+                        const uint32_t s2 = live ? scale_f16x2(sw, p & 3) : 0u;
+                        const uint4 cv = live ? raw.codes[i] : make_uint4(0, 0, 0, 0);
+                        uint8_t* blk = dst + (p >> 1) * kBlk;
+                        const int ch = 4 * (p & 1);
+                        *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch)) = widen8_cvt(cv.x, s2);
+                        *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 1)) = widen8_perm(cv.y, s2);
+                        *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 2)) = widen8_cvt(cv.z, s2);
+                        *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 3)) = widen8_perm(cv.w, s2);
+                    }
+                    if (hf) {
+#pragma unroll
+                        for (int i = 0; i < 8 / kPieces; ++i)
+                            *reinterpret_cast<uint4*>(dst + 8 * kBlk + sw128_off(my_row, my_piece + kPieces * i)) =
+                                live ? raw.rope[i] : make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.kfull[st][hf]);
+                }
+                if (!ok) break;
+                // the next chunk's rows into the registers, and where the one after lies
+                cur = nxt;
+                if (c + kProdGroups < nch) load_row(cur);
+                if (c + 2 * kProdGroups < nch) nxt = row_of(c + 2 * kProdGroups);
             }
-            const bool attended = my_row < chunk_valid(gcof(c));
-            if (attended && cur == nullptr) set_status(status, LCS_ERR_DEVICE, 602);
-            const bool live = attended && cur != nullptr;
-            bool ok = true;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                if (c >= 2 && !warp_wait(&bars.kempty[st][hf], par, status, 611 + hf)) {
-                    ok = false;
-                    break;
-                }
-                // piece p: codes 32 p .. 32 p + 31, 16-byte chunks 4 (p & 1) .. + 3 of column block p / 2.  A store's
-                // eight lanes differ in the row's low bits or (four rows a warp) in p & 1: eight bank groups.
-#pragma unroll
-                for (int i = hf * (8 / kPieces); i < (hf + 1) * (8 / kPieces); ++i) {
-                    const int p = my_piece + kPieces * i;
-                    const uint32_t sw = p < 8 ? (p < 4 ? raw.scales.x : raw.scales.y) : (p < 12 ? raw.scales.z : raw.scales.w);
-                    const uint32_t s2 = live ? scale_f16x2(sw, p & 3) : 0u;
-                    const uint4 cv = live ? raw.codes[i] : make_uint4(0, 0, 0, 0);
-                    uint8_t* blk = dst + (p >> 1) * kBlk;
-                    const int ch = 4 * (p & 1);
-                    *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch)) = widen8_cvt(cv.x, s2);
-                    *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 1)) = widen8_perm(cv.y, s2);
-                    *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 2)) = widen8_cvt(cv.z, s2);
-                    *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 3)) = widen8_perm(cv.w, s2);
-                }
-                if (hf) {
-#pragma unroll
-                    for (int i = 0; i < 8 / kPieces; ++i)
-                        *reinterpret_cast<uint4*>(dst + 8 * kBlk + sw128_off(my_row, my_piece + kPieces * i)) =
-                            live ? raw.rope[i] : make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.kfull[st][hf]);
-            }
-            if (!ok) break;
-            // the next chunk's rows into the registers, and where the one after lies
-            cur = nxt;
-            if (c + 1 < nch) load_row(cur);
-            if (c + 2 < nch) nxt = row_of(c + 2);
+            if ((st += kProdGroups) >= kStages) st -= kStages, ph ^= 1;
         }
         cp_async_wait<0>();
-    } else if (warp < kSoftWarps) {
-        // ---------------- softmax: warp w owns heads 16w .. + 15; lane l works on head 16w + (l & 15), on S columns
-        // 0-31 (lanes 0-15) or 32-63 (lanes 16-31)
-        const int head = warp * 16 + (lane & 15);
-        const int cbase = (lane < 16) ? 0 : 32;
+    } else {
+        // ---------------- softmax: warp w owns heads 16w .. + 15; lane l works on head 16w + (l & 15)
+        const int head = warp * 16 + (lane & 15), hi16 = lane >> 4;
         float m_used = -INFINITY, l_sum = 0.f;   // log2 domain; weights are 2^(s - m_used + kLift)
         const float sl2 = a.scale * kLog2e * bars.qscale[head];
+        if (nch > 0) {
+            // Q's dims 0 .. kTQ-1 into TMEM, both halves of the lanes
+#pragma unroll 2
+            for (int k = 0; k < kTQ / 64; ++k) {
+                uint4 v[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(q_block(k) + sw128_off(head, c));
+#pragma unroll
+                for (int c = 0; c < 8; c += 2) {
+                    const uint32_t o[8] = {v[c].x, v[c].y, v[c].z, v[c].w, v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
+                    tmem_st8(tmem_addr(tmem, warp * 32, kTmQ + 32 * k + 4 * c), o);
+                }
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.qfull);
+        }
         const uint32_t flip = sl2 < 0.f ? 0x80000000u : 0u;
         for (int c = 0; c < nch; ++c) {
-            const int st = c & 1;
-            if (!warp_wait(&bars.sfull[st], (uint32_t)((c >> 1) & 1), status, 620)) break;
+            const int pb = c & 1;
+            if (!warp_wait(&bars.sfull[pb], (uint32_t)((c >> 1) & 1), status, 620)) break;
             tc_fence_after();
-            uint32_t sv[32];
-            tmem_ld16x2_32(tmem_addr(t_s(st), warp * 32, 0), sv);
+            // S columns 0-23 (lanes 0-15) or 24-47 (lanes 16-31) of this lane's head
+            uint32_t sv[24];
+            const uint32_t ts = tmem_addr(tmem, warp * 32 + 16 * pb, kTmS);
+            tmem_ld16x2_16(ts, sv);
+            tmem_ld16x2_8(ts + 16, sv + 16);
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.sempty[st]);
+            if (lane == 0) mbar_arrive(&bars.sempty[pb]);
             // the maximum of scale * s is that of s (of -s for a negative scale) times |scale|
-            const int valid = chunk_valid(gcof(c)) - cbase;
+            const int valid = chunk_valid(gcof(c)) - 24 * hi16;
             float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (valid >= 32) {
+            if (valid >= 24) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(sv[j] ^ flip));
+                for (int j = 0; j < 24; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(sv[j] ^ flip));
             } else {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < 24; ++j)
                     if (j < valid) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(sv[j] ^ flip));
             }
             float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
@@ -704,27 +782,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 m_used = m_new;
             }
             const float off = m_used == -INFINITY ? 0.f : m_used - kLift;   // every score -inf: weights 0
-            // p to fp16 and into the RoPE block, 16 bytes at a time
-            uint8_t* pblk = stage_s + st * kStageBytes + 8 * kBlk;
             float ps[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t pk[24];   // P of the head's 48 rows, fp16 pairs
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                uint32_t pk[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int j = 8 * ch + 2 * q;
-                    float p0 = ex2(fmaf(__uint_as_float(sv[j]), sl2, -off));
-                    float p1 = ex2(fmaf(__uint_as_float(sv[j + 1]), sl2, -off));
-                    if (j >= valid) p0 = 0.f;   // columns past the chunk's rows weigh nothing
-                    if (j + 1 >= valid) p1 = 0.f;
-                    ps[q] += p0 + p1;
-                    pk[q] = pack_f16x2(p0, p1);
-                }
-                *reinterpret_cast<uint4*>(pblk + sw128_off(head, (cbase >> 3) + ch)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            for (int j = 0; j < 24; j += 2) {
+                float p0 = ex2(fmaf(__uint_as_float(sv[j]), sl2, -off));
+                float p1 = ex2(fmaf(__uint_as_float(sv[j + 1]), sl2, -off));
+                if (j >= valid) p0 = 0.f;   // columns past the chunk's rows weigh nothing
+                if (j + 1 >= valid) p1 = 0.f;
+                ps[(j >> 1) & 3] += p0 + p1;
+                const uint32_t own = pack_f16x2(p0, p1), other = __shfl_xor_sync(0xffffffffu, own, 16);
+                pk[j / 2] = hi16 ? other : own;
+                pk[12 + j / 2] = hi16 ? own : other;
             }
+            // P goes where P.V of chunk c - 2 read it
+            if (c >= 2 && !warp_wait(&bars.ofull[pb], (uint32_t)(((c - 2) >> 1) & 1), status, 623)) break;
+            const uint32_t tp = tmem_addr(tmem, warp * 32, kTmP + pb * (kChunk / 2));
+            tmem_st8(tp, pk);
+            tmem_st8(tp + 8, pk + 8);
+            tmem_st8(tp + 16, pk + 16);
             if (__any_sync(0xffffffffu, rescale)) {
                 // O may be written once the previous chunk's P.V is done
-                if (!warp_wait(&bars.ofull[(c - 1) & 1], (uint32_t)(((c - 1) >> 1) & 1), status, 621)) break;
+                if (!warp_wait(&bars.ofull[pb ^ 1], (uint32_t)(((c - 1) >> 1) & 1), status, 621)) break;
                 tc_fence_after();
                 const float f = rescale ? alpha : 1.f;
 #pragma unroll 1
@@ -737,33 +816,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int q = 0; q < 16; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * f);
                     tmem_st16(ta, ov);
                 }
-                tmem_st_wait();
-                tc_fence_before();
             }
-            fence_proxy_async_smem();
+            tmem_st_wait();
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.pfull[st]);
+            if (lane == 0) mbar_arrive(&bars.pfull[pb]);
             float psum = (ps[0] + ps[1]) + (ps[2] + ps[3]);
             psum += __shfl_xor_sync(0xffffffffu, psum, 16);
             l_sum = l_sum * alpha + psum;
         }
-        // ---- O.  Lane l of warp w holds the O row of head 16w + (l & 15), dims 0-255 (lanes 0-15) or 256-511
-        // (lanes 16-31).  The only split: normalised, staged through shared memory.  One of several: the
-        // partial and (m, l) as the lanes hold them ([quarter][4 dims][lane], 512 bytes a store).
         if (nch > 0) warp_wait(&bars.odone, 0, status, 622);
+        if (lane < 16) {
+            const float m = l_sum > 0.f ? m_used - kLift : -INFINITY;
+            bars.inv_l[head] = l_sum > 0.f ? 1.f / l_sum : 0.f;
+            if (only) {
+                if (a.lse != nullptr && head < nh)
+                    a.lse[(int64_t)g * a.H + h0 + head] = l_sum > 0.f ? (m + log2f(l_sum)) / kLog2e : -INFINITY;
+            } else {
+                float* ml = part_ml + ((int64_t)(unit * splits + sp) * kH + head) * 2;
+                ml[0] = m;
+                ml[1] = l_sum;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    // ---- O, eight warps: lane l of warp w holds the O row of head 16 (w & 3) + (l & 15), dims 0-127 (+ 128
+    // for w >= 4, + 256 for l >= 16).  The only split: normalised, staged through shared memory.  One of
+    // several: the partial as the lanes hold it ([quarter][4 dims][lane], 512 bytes a store).
+    if (warp < 8) {
         tc_fence_after();
-        const bool only = splits == 1;
-        const float fs = only ? ((l_sum > 0.f) ? 1.f / l_sum : 0.f) : 1.f;
+        const int quarter = warp & 3, head = quarter * 16 + (lane & 15);
+        const float fs = only ? bars.inv_l[head] : 1.f;
         const int dim0 = (lane < 16) ? 0 : 256;
         const bool f32 = a.out_dtype == LCS_F32;
         uint8_t* rowp = stage_s + head * (f32 ? kOPitchF32 : kOPitchBF16);
-        float4* gpart = reinterpret_cast<float4*>(part_o) + ((int64_t)(unit * splits + sp) * 4 + warp) * (64 * 32) + lane;
+        float4* gpart = reinterpret_cast<float4*>(part_o) + ((int64_t)(unit * splits + sp) * 4 + quarter) * (64 * 32) + lane;
 #pragma unroll 1
-        for (int j0 = 0; j0 < 16; j0 += 4) {
+        for (int j0 = (warp >> 2) * 8; j0 < (warp >> 2) * 8 + 8; j0 += 4) {
             uint32_t ov[4][16];
             if (nch > 0) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) tmem_ld16(tmem_addr(tmem, warp * 32, (j0 + u) * 16), ov[u]);
+                for (int u = 0; u < 4; ++u) tmem_ld16(tmem_addr(tmem, quarter * 32, (j0 + u) * 16), ov[u]);
                 tmem_ld_wait();
             } else {
 #pragma unroll
@@ -793,22 +887,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
         }
-        if (lane < 16) {
-            const float m = l_sum > 0.f ? m_used - kLift : -INFINITY;
-            if (only) {
-                if (a.lse != nullptr && head < nh)
-                    a.lse[(int64_t)g * a.H + h0 + head] = l_sum > 0.f ? (m + log2f(l_sum)) / kLog2e : -INFINITY;
-            } else {
-                float* ml = part_ml + ((int64_t)(unit * splits + sp) * kH + head) * 2;
-                ml[0] = m;
-                ml[1] = l_sum;
-            }
-        }
     }
-
     tc_fence_before();
     __syncthreads();
-    if (splits == 1) {
+    if (only) {
         // the staged output rows with coalesced 16-byte stores
         const bool f32 = a.out_dtype == LCS_F32;
         const int pitch = f32 ? kOPitchF32 : kOPitchBF16;
@@ -821,7 +903,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     }
 #if defined(__CUDA_ARCH__)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the split combine
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the split merge
 #endif
     if (warp == kWarpQK) {
         tc_fence_after();
