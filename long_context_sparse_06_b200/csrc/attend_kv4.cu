@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
 //    above, where 4-bit rows end at 2688.
 //  * Shared memory is what an SM runs out of: its bandwidth (an MMA with both operands in it takes
 //    4 KB per 32 cycles) and its size (a chunk is the K-major B of Q.K^T and the MN-major B of P.V).
-//    So P and 320 of Q's dims are A operands in TMEM, in the lanes of the accumulator they
-//    meet: S of even and odd chunks and O's dims 0-255 and 256-511 use the two halves of every 32
-//    lanes, and Q and P are kept in both.  That leaves room for three stages of 48 rows, each
+//    So 384 of Q's dims are an A operand in TMEM, in the lanes of the accumulator they meet: S of
+//    even and of odd chunks uses the two halves of every 32 lanes (as O's dims 0-255 and
+//    256-511 do), and Q is kept in both.  That leaves room for three stages of 48 rows, each
 //    released in two halves of the columns as P.V leaves them: widening, Q.K^T, softmax and P.V of
 //    different chunks run side by side (two stages of 64 rows took 3400 cycles per 64 rows, where
 //    each step was the others' wait).
@@ -229,7 +229,7 @@ constexpr int kH = 64, kD = 576, kDv = 512, kChunk = 48, kStages = 3;
 constexpr int kBlk = kChunk * 128;            // one SW128 column block of a chunk: 48 rows x 128 B
 constexpr int kStageBytes = 9 * kBlk;         // 54 KB
 constexpr int kQBlk = kH * 128;               // one SW128 column block of Q
-constexpr int kTQ = 320;                      // Q's dims 0 .. kTQ-1 in TMEM, the others in shared memory
+constexpr int kTQ = 384;                      // Q's dims 0 .. kTQ-1 in TMEM, the others in shared memory
 constexpr int kQBytes = (9 - kTQ / 64) * kQBlk;
 constexpr int kSoftWarps = 4, kProdWarps = 6, kProdGroups = 2;
 constexpr int kWarpQK = kSoftWarps + kProdGroups * kProdWarps, kWarpPV = kWarpQK + 1, kTcWarps = kWarpPV + 1;
@@ -238,15 +238,16 @@ constexpr int kRowsPerWarp = kChunk / kProdWarps;             // rows of a chunk
 constexpr int kPieces = 32 / kRowsPerWarp;                    // lanes that share a row
 static_assert(kRowsPerWarp == 8, "a store's eight lanes hold eight rows: eight bank groups");
 constexpr int kHalfBlocks = 4;                // column blocks of a stage's first half
-constexpr size_t kTcSmem = 1024 + kQBytes + kStages * kStageBytes;
+constexpr int kPBytes = kH * 128;             // P: 64 heads x 48 rows, fp16, K-major SW128 rows of 128 B
+constexpr size_t kTcSmem = 1024 + kQBytes + kStages * kStageBytes + 2 * kPBytes;
 constexpr int kMaxSplits = 64;
 constexpr int kOPitchF32 = kDv * 4 + 16;      // staged O rows (padded)
 constexpr int kOPitchBF16 = kDv * 2 + 16;
 static_assert(kH * kOPitchF32 <= kStages * kStageBytes, "staged O fits in the stages");
-static_assert(kTQ / 64 * kQBlk <= kStageBytes, "Q's TMEM part passes through the last stage");
-// TMEM columns: O, S (even chunks in lanes 0-15 of each 32, odd ones in lanes 16-31), P of even and
-// of odd chunks, Q (the last three twice, for both halves of the lanes).
-constexpr uint32_t kTmS = 256, kTmP = kTmS + kChunk, kTmQ = kTmP + 2 * (kChunk / 2), kHi16 = 16u << 16;
+static_assert(kTQ / 64 * kQBlk <= kStageBytes && kH * 128 == kQBlk, "Q's TMEM part passes through the last stage");
+// TMEM columns: O, S (even chunks in lanes 0-15 of each 32, odd ones in lanes 16-31), Q (twice, for
+// both halves of the lanes).
+constexpr uint32_t kTmS = 256, kTmQ = kTmS + kChunk, kHi16 = 16u << 16;
 static_assert(kTmQ + kTQ / 2 <= 512, "TMEM columns");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.0f;              // log2 of the tolerated growth before O is rescaled
@@ -435,6 +436,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* q_s = smem;
     uint8_t* stage_s = smem + kQBytes;
+    uint8_t* p_s = stage_s + kStages * kStageBytes;
 
     // values that steer whole warps come from lane 0, so that the compiler keeps them (and what the MMA
     // issue derives from them) in uniform registers
@@ -547,7 +549,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     cp_async_wait<0>();
     __syncthreads();
-    // ---- Q scaled by 2^e in place, a warp per head; content to fp16
+    // ---- Q scaled by 2^e (and by the sign of the scale) in place, a warp per head; content to fp16
+    const uint32_t neg = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll 1
     for (int h = warp; h < kH; h += kTcWarps) {
         const uint32_t at = sw128_off(h, lane & 7);   // chunks lane, lane + 32, lane + 64
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int ex = (int)(mag >> 7) - 127;               // of the largest element (subnormals: -127)
         int e = mag == 0 || mag >= 0x7F80u ? 0 : 14 - ex;   // zero, infinite or NaN heads stay as they are
         e = e > 126 ? 126 : e;
-        const uint32_t up2 = (uint32_t)(127 + e) * 0x00800080u;
+        const uint32_t up2 = (uint32_t)(127 + e) * 0x00800080u | neg;
         if (lane == 0) bars.qscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
         *x0 = make_uint4(bf16x2_to_f16x2(bf16x2_mul(v0.x, up2)), bf16x2_to_f16x2(bf16x2_mul(v0.y, up2)),
                          bf16x2_to_f16x2(bf16x2_mul(v0.z, up2)), bf16x2_to_f16x2(bf16x2_mul(v0.w, up2)));
@@ -632,17 +635,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         constexpr uint32_t id = idesc_f16(idesc_bf16(64, 256, false, true));
         const uint64_t v_desc = sw128_desc(smem_u32(stage_s), kBlk, 1024);
         const uint32_t va0 = (uint32_t)v_desc, hi = (uint32_t)(v_desc >> 32);
+        const uint32_t pa0 = (uint32_t)sw128_desc(smem_u32(p_s), 16, 1024);
         int st = 0;
         for (int c = 0; c < nch; ++c) {
             if (!warp_wait(&bars.pfull[c & 1], (uint32_t)((c >> 1) & 1), status, 608)) break;
             tc_fence_after();
             const uint32_t va = va0 + (uint32_t)((st * kStageBytes) >> 4);
-            const uint32_t pt = tmem + kTmP + (uint32_t)(c & 1) * (kChunk / 2);
+            const uint32_t pa = pa0 + (uint32_t)(((c & 1) * kPBytes) >> 4);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
                 for (int kk = 0; kk < kChunk / 16; ++kk)
-                    mma_ts_if(on, tmem + (half ? kHi16 : 0u), pt + (half ? kHi16 : 0u) + 8 * kk,
+                    mma_ss_if(on, tmem + (half ? kHi16 : 0u), pa + (uint32_t)((kk * 32) >> 4),
                               va + (uint32_t)((half * kHalfBlocks * kBlk + kk * 2048) >> 4), hi, id, (c | kk) ? 1u : 0u);
                 // dims 0-255 read column blocks 0-3; blocks 4-8 are released after the rest
                 commit_if(on, &bars.kempty[st][half]);
@@ -727,7 +731,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ---------------- softmax: warp w owns heads 16w .. + 15; lane l works on head 16w + (l & 15)
         const int head = warp * 16 + (lane & 15), hi16 = lane >> 4;
         float m_used = -INFINITY, l_sum = 0.f;   // log2 domain; weights are 2^(s - m_used + kLift)
-        const float sl2 = a.scale * kLog2e * bars.qscale[head];
+        const float sl2 = fabsf(a.scale) * kLog2e * bars.qscale[head];
         if (nch > 0) {
             // Q's dims 0 .. kTQ-1 into TMEM, both halves of the lanes
 #pragma unroll 2
@@ -746,7 +750,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.qfull);
         }
-        const uint32_t flip = sl2 < 0.f ? 0x80000000u : 0u;
         for (int c = 0; c < nch; ++c) {
             const int pb = c & 1;
             if (!warp_wait(&bars.sfull[pb], (uint32_t)((c >> 1) & 1), status, 620)) break;
@@ -760,19 +763,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.sempty[pb]);
-            // the maximum of scale * s is that of s (of -s for a negative scale) times |scale|
+            // (scale and 2^-e are not negative: the maximum of the scores is that of s, times them)
             const int valid = chunk_valid(gcof(c)) - 24 * hi16;
-            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (valid >= 24) {
-#pragma unroll
-                for (int j = 0; j < 24; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(sv[j] ^ flip));
-            } else {
+            if (valid < 24) {
 #pragma unroll
                 for (int j = 0; j < 24; ++j)
-                    if (j < valid) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(sv[j] ^ flip));
+                    if (j >= valid) sv[j] = 0xFF800000u;   // -inf: no part of the maximum
             }
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 24; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(sv[j]));
             float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * fabsf(sl2);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * sl2;
             float alpha = 1.f;
             bool rescale = false;
             if (mx > m_used + kRescale || m_used == -INFINITY) {
@@ -782,25 +784,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 m_used = m_new;
             }
             const float off = m_used == -INFINITY ? 0.f : m_used - kLift;   // every score -inf: weights 0
-            float ps[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t pk[24];   // P of the head's 48 rows, fp16 pairs
 #pragma unroll
-            for (int j = 0; j < 24; j += 2) {
-                float p0 = ex2(fmaf(__uint_as_float(sv[j]), sl2, -off));
-                float p1 = ex2(fmaf(__uint_as_float(sv[j + 1]), sl2, -off));
-                if (j >= valid) p0 = 0.f;   // columns past the chunk's rows weigh nothing
-                if (j + 1 >= valid) p1 = 0.f;
-                ps[(j >> 1) & 3] += p0 + p1;
-                const uint32_t own = pack_f16x2(p0, p1), other = __shfl_xor_sync(0xffffffffu, own, 16);
-                pk[j / 2] = hi16 ? other : own;
-                pk[12 + j / 2] = hi16 ? own : other;
+            for (int j = 0; j < 24; ++j) sv[j] = __float_as_uint(ex2(fmaf(__uint_as_float(sv[j]), sl2, -off)));
+            if (valid < 24) {   // columns past the chunk's rows weigh nothing (0 times -inf above is no number)
+#pragma unroll
+                for (int j = 0; j < 24; ++j)
+                    if (j >= valid) sv[j] = 0u;
             }
+            float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 24; ++j) ps[j & 3] += __uint_as_float(sv[j]);
             // P goes where P.V of chunk c - 2 read it
             if (c >= 2 && !warp_wait(&bars.ofull[pb], (uint32_t)(((c - 2) >> 1) & 1), status, 623)) break;
-            const uint32_t tp = tmem_addr(tmem, warp * 32, kTmP + pb * (kChunk / 2));
-            tmem_st8(tp, pk);
-            tmem_st8(tp + 8, pk + 8);
-            tmem_st8(tp + 16, pk + 16);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    pk[q] = pack_f16x2(__uint_as_float(sv[8 * k + 2 * q]), __uint_as_float(sv[8 * k + 2 * q + 1]));
+                *reinterpret_cast<uint4*>(p_s + pb * kPBytes + sw128_off(head, 3 * hi16 + k)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
             if (__any_sync(0xffffffffu, rescale)) {
                 // O may be written once the previous chunk's P.V is done
                 if (!warp_wait(&bars.ofull[pb ^ 1], (uint32_t)(((c - 1) >> 1) & 1), status, 621)) break;
@@ -816,9 +819,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int q = 0; q < 16; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * f);
                     tmem_st16(ta, ov);
                 }
+                tmem_st_wait();
+                tc_fence_before();
             }
-            tmem_st_wait();
-            tc_fence_before();
+            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.pfull[pb]);
             float psum = (ps[0] + ps[1]) + (ps[2] + ps[3]);
