@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
 
 // ----------------------------------------------------------- tensor-core path
 // bf16 queries, d_c = 512, d_r = 64.  One CTA (18 warps) per (query, tile of 64 heads, split of its
-// row list); the row list is the window rows, padded to whole chunks of 48, then the selected or
-// available entries; chunk i goes to split i mod splits.
+// row list); the row list is the selected or available entries, padded to whole chunks of 48, then
+// the window rows; chunk i goes to split i mod splits.
 //
 //   S [64 heads x 48 rows] = Q [64 x 576] . K_chunk^T,  O [64 x 512] += P [64 x 48] . V_chunk
 //
@@ -487,21 +487,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         cp_async_commit();
     }
-    // ... and the producers' first rows.  Which of a chunk's rows are attended is known later (the
-    // selection's length): rows behind it are dropped when they are widened.
-    const Kv4Window wp = kv4_window(a, g, b);
-    const int64_t n = kv4_entries(a, b, status);
-    const int nwc = (int)((wp.n + kChunk - 1) / kChunk);
-    const int nwl = uni(sp < nwc ? (nwc - sp + splits - 1) / splits : 0);   // this split's window chunks, first
+    // ... and the producers' first rows.  A group takes every other chunk.  How many entries there are, and
+    // which of a chunk's rows are attended (the selection's length), is known later: rows past it
+    // are dropped when they are widened.
     const int32_t* sel = a.idx != nullptr ? a.idx + (int64_t)g * a.k : nullptr;
-    const int most = sel != nullptr ? a.k : (int)kv4_avail(a, g, n);
+    const int held = (int)(a.max_blocks * a.be);   // entries that the table can hold
     auto gcof = [&](int c) -> int { return sp + splits * c; };
     const int my_row = pw * kRowsPerWarp + lane % kRowsPerWarp, my_piece = lane / kRowsPerWarp;
-    auto row_of = [&](int c) -> const uint8_t* {   // this lane's row of local chunk c, null if there is none
-        const int j = (gcof(c) - nwc) * kChunk + my_row;
-        if (j >= most) return nullptr;
+    auto row_of = [&](int c, int lim) -> const uint8_t* {   // this lane's row of local chunk c, null if there is none
+        const int j = gcof(c) * kChunk + my_row;
+        if (j >= (sel != nullptr ? a.k : lim)) return nullptr;
         const int e = sel != nullptr ? __ldg(sel + j) : j;
-        return e >= 0 && e < n ? kv4_row(a, b, e) : nullptr;
+        return e >= 0 && e < lim ? kv4_row(a, b, e) : nullptr;
     };
     RawRow raw;
     auto load_row = [&](const uint8_t* src) {
@@ -514,29 +511,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             raw.scales = __ldg(reinterpret_cast<const uint4*>(src) + 24);
         }
     };
-    // window chunk c of this split into its stage st: bf16 rows by 16-byte cp.async, zeros past the last row
-    auto load_window = [&](int c, int st) {
-        uint8_t* dst = stage_s + st * kStageBytes;
-        const int64_t w0 = (int64_t)gcof(c) * kChunk;
-        const uint8_t* src = static_cast<const uint8_t*>(a.win) + ((int64_t)b * a.Tw + wp.lo + w0) * (kD * 2);
-#pragma unroll 1
-        for (int i = 0; i < kRowsPerWarp; ++i) {
-            const int r = pw * kRowsPerWarp + i;
-            const bool valid = w0 + r < wp.n;
-            for (int ch = lane; ch < 72; ch += 32)
-                cp_async_16(dst + (ch >> 3) * kBlk + sw128_off(r, ch & 7), src + (valid ? r * (kD * 2) + ch * 16 : 0), valid);
-        }
-        cp_async_commit();
-    };
-    // a group's first compressed chunk, the next one it takes being two on
-    const int first = nwl + ((nwl ^ pg) & 1);
     const uint8_t *cur = nullptr, *nxt = nullptr;
     if (producer) {
-        cur = row_of(first);
+        cur = row_of(pg, held);
         load_row(cur);
-        if (pg < nwl) load_window(pg, pg);
-        nxt = row_of(first + 2);
     }
+    const Kv4Window wp = kv4_window(a, g, b);
+    const int64_t n = kv4_entries(a, b, status);
+    const int most = sel != nullptr ? a.k : (int)kv4_avail(a, g, n);
+    if (producer) nxt = row_of(pg + kProdGroups, (int)(sel != nullptr ? n : most));
     // ---- selection length (CSA: the valid prefix of idx): a minimum per warp, joined below
     if (sel != nullptr) {
         int first_bad = a.k;
@@ -551,7 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     // ---- Q scaled by 2^e (and by the sign of the scale) in place, a warp per head; content to fp16
     const uint32_t neg = a.scale < 0.f ? 0x80008000u : 0u;
-#pragma unroll 1
+#pragma unroll 2
     for (int h = warp; h < kH; h += kTcWarps) {
         const uint32_t at = sw128_off(h, lane & 7);   // chunks lane, lane + 32, lane + 64
         uint4* x0 = reinterpret_cast<uint4*>(q_block(lane >> 3) + at);
@@ -585,11 +568,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // an index past the entries ended it; -1 is the padding
         if (threadIdx.x == 0 && nsel < a.k && __ldg(sel + nsel) >= 0) set_status(status, LCS_ERR_DEVICE, 603);
     }
-    const int nch_all = nwc + (nsel + kChunk - 1) / kChunk;
-    const int nch = uni(sp < nch_all ? (nch_all - sp + splits - 1) / splits : 0);   // this split's chunks
-    auto chunk_valid = [&](int gc) -> int {
-        const int64_t v = gc < nwc ? wp.n - (int64_t)gc * kChunk : (int64_t)nsel - (int64_t)(gc - nwc) * kChunk;
-        return (int)(v < kChunk ? v : kChunk);
+    // this split's chunks, and the compressed ones among them, which come first
+    const int ncc_all = (nsel + kChunk - 1) / kChunk, nch_all = ncc_all + (int)((wp.n + kChunk - 1) / kChunk);
+    const int nch = uni(sp < nch_all ? (nch_all - sp + splits - 1) / splits : 0);
+    const int ncc = uni(sp < ncc_all ? (ncc_all - sp + splits - 1) / splits : 0);
+    auto chunk_valid = [&](int c) -> int {   // rows of local chunk c
+        const int gc = gcof(c);
+        const int v = c < ncc ? nsel - gc * kChunk : (int)wp.n - (gc - ncc_all) * kChunk;
+        return v < kChunk ? v : kChunk;
     };
     const bool only = splits == 1;
 
@@ -663,17 +649,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint8_t* dst = stage_s + st * kStageBytes;
             // Q's TMEM part leaves the last stage before its first rows come in
             if (c == kStages - 1 && !warp_wait(&bars.qfull, 0, status, 613)) break;
-            if (c < nwl) {
+            if (c >= ncc) {
+                // window chunk: bf16 rows by 16-byte cp.async, zeros past the last row; content to fp16 in place
                 if (c >= kStages && (!warp_wait(&bars.kempty[st][0], ph, status, 609) ||
                                      !warp_wait(&bars.kempty[st][1], ph, status, 610)))
                     break;
-                if (c != pg) load_window(c, st);   // the first is on its way
+                const int w0 = (gcof(c) - ncc_all) * kChunk;
+                const uint8_t* src = static_cast<const uint8_t*>(a.win) + ((int64_t)b * a.Tw + wp.lo + w0) * (kD * 2);
+                const uint32_t r0 = pw * kRowsPerWarp;
+#pragma unroll 2
+                for (int i = lane; i < kRowsPerWarp * 72; i += 32) {
+                    const uint32_t r = r0 + (uint32_t)i / 72u, ch = (uint32_t)i % 72u;
+                    const bool valid = w0 + (int)r < (int)wp.n;
+                    cp_async_16(dst + (ch >> 3) * kBlk + sw128_off(r, ch & 7), src + (valid ? r * (kD * 2) + ch * 16 : 0), valid);
+                }
+                cp_async_commit();
                 cp_async_wait<0>();
                 __syncwarp();
-                // content to fp16 in place (a lane's own copies): this warp's rows, 64 chunks each
 #pragma unroll 4
                 for (int i = lane; i < kRowsPerWarp * 64; i += 32) {
-                    uint4* x = reinterpret_cast<uint4*>(dst + ((i & 63) >> 3) * kBlk + sw128_off(pw * kRowsPerWarp + (i >> 6), i & 7));
+                    uint4* x = reinterpret_cast<uint4*>(dst + ((i & 63) >> 3) * kBlk + sw128_off(r0 + (i >> 6), i & 7));
                     const uint4 v = *x;
                     *x = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
                 }
@@ -684,7 +679,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     mbar_arrive(&bars.kfull[st][1]);
                 }
             } else {
-                const bool attended = my_row < chunk_valid(gcof(c));
+                const bool attended = my_row < chunk_valid(c);
                 if (attended && cur == nullptr) set_status(status, LCS_ERR_DEVICE, 602);
                 const bool live = attended && cur != nullptr;
                 bool ok = true;
@@ -719,10 +714,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (lane == 0) mbar_arrive(&bars.kfull[st][hf]);
                 }
                 if (!ok) break;
-                // the next chunk's rows into the registers, and where the one after lies
+                // the group's next chunk's rows into the registers, and where the one after lies
                 cur = nxt;
-                if (c + kProdGroups < nch) load_row(cur);
-                if (c + 2 * kProdGroups < nch) nxt = row_of(c + 2 * kProdGroups);
+                if (c + kProdGroups < ncc) load_row(cur);
+                if (c + 2 * kProdGroups < ncc) nxt = row_of(c + 2 * kProdGroups, (int)(sel != nullptr ? n : most));
             }
             if ((st += kProdGroups) >= kStages) st -= kStages, ph ^= 1;
         }
@@ -764,7 +759,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.sempty[pb]);
             // (scale and 2^-e are not negative: the maximum of the scores is that of s, times them)
-            const int valid = chunk_valid(gcof(c)) - 24 * hi16;
+            const int valid = chunk_valid(c) - 24 * hi16;
             if (valid < 24) {
 #pragma unroll
                 for (int j = 0; j < 24; ++j)
