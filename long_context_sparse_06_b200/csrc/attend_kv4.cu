@@ -240,7 +240,7 @@ static_assert(kRowsPerWarp == 8, "a store's eight lanes hold eight rows: eight b
 constexpr int kHalfBlocks = 4;                // column blocks of a stage's first half
 constexpr int kPBytes = kH * 128;             // P: 64 heads x 48 rows, fp16, K-major SW128 rows of 128 B
 constexpr size_t kTcSmem = 1024 + kQBytes + kStages * kStageBytes + 2 * kPBytes;
-constexpr int kMaxSplits = 64;
+constexpr int kMaxSplits = 64, kMaxCluster = 16;
 constexpr int kOPitchF32 = kDv * 4 + 16;      // staged O rows (padded)
 constexpr int kOPitchBF16 = kDv * 2 + 16;
 static_assert(kH * kOPitchF32 <= kStages * kStageBytes, "staged O fits in the stages");
@@ -428,8 +428,66 @@ struct RawRow {
     uint4 codes[16 / kPieces], rope[8 / kPieces], scales;
 };
 
+// Split partials lie as the attention's lanes held them: per unit and split 256 rows of 32 lanes x 16
+// bytes; row 64 quarter + j holds 4 dims of 16 heads in either half of the output (lane l: head 16
+// quarter + (l & 15), dims 4 j .. + 3, + 256 for l >= 16).  One warp merges the R rows of task t (of
+// 256 / R): quarter t & 3, j = R (t >> 2) .. + R - 1.  A lane forms its head's weights 2^(m_s - M)
+// itself, in split order with a running maximum, S splits' loads in flight.
+template <int R, int S>
+__device__ __forceinline__ void merge_task(const AttendKv4Args& a, int tiles, int splits, int unit, int t,
+                                           const float* part_o, const float* part_ml) {
+    const int lane = threadIdx.x & 31, quarter = t & 3, j0 = R * (t >> 2);
+    const int g = tiles == 2 ? unit >> 1 : unit, in_tile = 16 * quarter + (lane & 15);
+    const int head = (tiles == 2 ? (unit & 1) * kH : 0) + in_tile;
+    const float4* src = reinterpret_cast<const float4*>(part_o) + ((int64_t)unit * splits * 256 + 64 * quarter + j0) * 32 + lane;
+    const float2* ml = reinterpret_cast<const float2*>(part_ml) + (int64_t)unit * splits * kH + in_tile;
+    float M = -INFINITY, L = 0.f;
+    float4 acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < splits; s0 += S) {
+        float4 v[R][S];
+        float2 x[S];
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+            const int s = min(s0 + k, splits - 1);   // (past the last one: read again, weight 0)
+            x[k] = __ldcg(ml + (int64_t)s * kH);
+#pragma unroll
+            for (int r = 0; r < R; ++r) v[r][k] = __ldcg(src + ((int64_t)s * 256 + r) * 32);
+        }
+        float m = M;
+#pragma unroll
+        for (int k = 0; k < S; ++k) m = fmaxf(m, x[k].x);
+        const float f = L > 0.f ? exp2f(M - m) : 0.f;
+        M = m;
+        L *= f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r] = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+            const float e = s0 + k < splits && x[k].y > 0.f ? exp2f(x[k].x - m) : 0.f;   // no rows, no weight
+            L += x[k].y * e;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                acc[r] = make_float4(acc[r].x + v[r][k].x * e, acc[r].y + v[r][k].y * e, acc[r].z + v[r][k].z * e,
+                                     acc[r].w + v[r][k].w * e);
+        }
+    }
+    if (head >= a.H) return;
+    const float iv = L > 0.f ? 1.f / L : 0.f;
+    const int64_t at = ((int64_t)g * a.H + head) * kDv + (lane < 16 ? 0 : 256) + 4 * j0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float4 o = make_float4(acc[r].x * iv, acc[r].y * iv, acc[r].z * iv, acc[r].w * iv);
+        if (a.out_dtype == LCS_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + 4 * r) = o;
+        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + 4 * r) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    }
+    if (a.lse != nullptr && j0 == 0 && lane < 16)
+        a.lse[(int64_t)g * a.H + head] = L > 0.f ? (M + log2f(L)) / kLog2e : -INFINITY;
+}
+
 __global__ void __launch_bounds__(kTcThreads, 1)
-    attend_kv4_tc_kernel(const AttendKv4Args a, int tiles, int splits, float* __restrict__ part_o,
+    attend_kv4_tc_kernel(const AttendKv4Args a, int tiles, int splits, int clustered, float* __restrict__ part_o,
                          float* __restrict__ part_ml, int* status) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ TcBars bars;
@@ -550,10 +608,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         e = e > 126 ? 126 : e;
         const uint32_t up2 = (uint32_t)(127 + e) * 0x00800080u | neg;
         if (lane == 0) bars.qscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
-        *x0 = make_uint4(bf16x2_to_f16x2(bf16x2_mul(v0.x, up2)), bf16x2_to_f16x2(bf16x2_mul(v0.y, up2)),
-                         bf16x2_to_f16x2(bf16x2_mul(v0.z, up2)), bf16x2_to_f16x2(bf16x2_mul(v0.w, up2)));
-        *x1 = make_uint4(bf16x2_to_f16x2(bf16x2_mul(v1.x, up2)), bf16x2_to_f16x2(bf16x2_mul(v1.y, up2)),
-                         bf16x2_to_f16x2(bf16x2_mul(v1.z, up2)), bf16x2_to_f16x2(bf16x2_mul(v1.w, up2)));
+        auto half8 = [&](uint4 v) {
+            auto half2 = [&](uint32_t w) {
+                w = bf16x2_mul(w, up2);
+                return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+            };
+            return make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+        };
+        *x0 = half8(v0);
+        *x1 = half8(v1);
         if (lane < 8)
             *x2 = make_uint4(bf16x2_mul(v2.x, up2), bf16x2_mul(v2.y, up2), bf16x2_mul(v2.z, up2), bf16x2_mul(v2.w, up2));
     }
@@ -578,6 +641,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return v < kChunk ? v : kChunk;
     };
     const bool only = splits == 1;
+#if defined(__CUDA_ARCH__)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the split merge: it may come in and wait
+#endif
 
     if (warp == kWarpQK) {
         // ---------------- Q.K^T issue
@@ -901,102 +967,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             *reinterpret_cast<uint4*>(gout + off) = *reinterpret_cast<const uint4*>(stage_s + h * pitch + cb);
         }
     }
-#if defined(__CUDA_ARCH__)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the split merge
-#endif
+    if (clustered) {
+        // a unit's splits are one cluster: its barrier orders the partials, each CTA merges every splits-th task
+        cluster_sync_all();
+        const int t0 = sp + splits * warp, dt = splits * kTcWarps;
+        if (splits <= 2)
+            for (int t = t0; t < 64; t += dt) merge_task<4, 2>(a, tiles, splits, unit, t, part_o, part_ml);
+        else if (splits <= 4)
+            for (int t = t0; t < 128; t += dt) merge_task<2, 4>(a, tiles, splits, unit, t, part_o, part_ml);
+        else
+            for (int t = t0; t < 256; t += dt) merge_task<1, 8>(a, tiles, splits, unit, t, part_o, part_ml);
+    }
     if (warp == kWarpQK) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
 }
 
-// Merges the split partials.  A CTA (8 warps) takes 16 heads of one unit (quarter = the softmax warp
-// that wrote them) and 32 dims of either half: a warp's lanes read 512 bytes of each split as they
-// were written, in split order, eight splits in flight; the weights 2^(m_s - M) and 1/L come from
-// one warp per two heads; the results go out through shared memory, 32 dims of a head together.
+// Merges the split partials of a launch whose splits are no clusters: a warp per task.
 constexpr int kMergeThreads = 256;
 __global__ void __launch_bounds__(kMergeThreads)
-    kv4_merge_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml, int splits, int H, int tiles,
-                     void* __restrict__ out, int out_dtype, float* __restrict__ lse) {
-    __shared__ float fac[16][kMaxSplits + 1];
-    __shared__ float inv_l[16];
-    __shared__ float o_s[32][33];
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int part = blockIdx.x & 7, quarter = (blockIdx.x >> 3) & 3;   // dims 32 part .. + 31 of both halves
-    const int unit = blockIdx.x >> 5;
-    const int g = tiles == 2 ? unit >> 1 : unit, h0 = (tiles == 2 ? (unit & 1) * kH : 0) + 16 * quarter;
+    kv4_merge_kernel(const AttendKv4Args a, int tiles, int splits, const float* __restrict__ part_o,
+                     const float* __restrict__ part_ml) {
+    const int w = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
 #if defined(__CUDA_ARCH__)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 #endif
-    if (h0 >= H) return;
-    const float4* src = reinterpret_cast<const float4*>(part_o) +
-                        (((int64_t)unit * splits * 4 + quarter) * 64 + 8 * part + warp) * 32 + lane;
-    constexpr int kFly = 8;
-    float4 v[kFly];
-#pragma unroll
-    for (int k = 0; k < kFly; ++k)
-        if (k < splits) v[k] = __ldcg(src + (int64_t)k * (4 * 64 * 32));
-    for (int i = 2 * warp; i < 2 * warp + 2; ++i) {
-        float2 ml[2];
-        float M = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int s = lane + 32 * k;
-            ml[k] = make_float2(-INFINITY, 0.f);
-            if (s < splits)
-                ml[k] = __ldcg(reinterpret_cast<const float2*>(part_ml) + ((int64_t)unit * splits + s) * kH + 16 * quarter + i);
-            M = fmaxf(M, ml[k].x);
-        }
-        M = warp_max(M);
-        float L = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float e = ml[k].y > 0.f ? exp2f(ml[k].x - M) : 0.f;
-            if (lane + 32 * k < splits) fac[i][lane + 32 * k] = e;
-            L += ml[k].y * e;
-        }
-        L = warp_sum(L);   // a fixed tree
-        if (lane == 0) {
-            inv_l[i] = L > 0.f ? 1.f / L : 0.f;
-            if (lse != nullptr && part == 0 && h0 + i < H)
-                lse[(int64_t)g * H + h0 + i] = L > 0.f ? (M + log2f(L)) / kLog2e : -INFINITY;
-        }
-    }
-    __syncthreads();
-    const int i = lane & 15;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < splits; s0 += kFly) {
-#pragma unroll
-        for (int k = 0; k < kFly; ++k)
-            if (s0 + k < splits) {
-                const float e = fac[i][s0 + k];
-                acc.x += v[k].x * e;
-                acc.y += v[k].y * e;
-                acc.z += v[k].z * e;
-                acc.w += v[k].w * e;
-            }
-#pragma unroll
-        for (int k = 0; k < kFly; ++k)
-            if (s0 + kFly + k < splits) v[k] = __ldcg(src + (int64_t)(s0 + kFly + k) * (4 * 64 * 32));
-    }
-    const float iv = inv_l[i];
-    o_s[lane][4 * warp] = acc.x * iv;
-    o_s[lane][4 * warp + 1] = acc.y * iv;
-    o_s[lane][4 * warp + 2] = acc.z * iv;
-    o_s[lane][4 * warp + 3] = acc.w * iv;
-    __syncthreads();
+    merge_task<1, 16>(a, tiles, splits, w >> 8, w & 255, part_o, part_ml);
 #if defined(__CUDA_ARCH__)
     // the partials are read: the next kernel of the stream may be set up
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #endif
-    // row r of o_s: head r & 15, dims (r < 16 ? 0 : 256) + 32 part + column
-    const int r = t >> 3, c4 = (t & 7) * 4;
-    if (h0 + (r & 15) < H) {
-        const int64_t at = ((int64_t)g * H + h0 + (r & 15)) * kDv + (r < 16 ? 0 : 256) + 32 * part + c4;
-        const float x = o_s[r][c4], y = o_s[r][c4 + 1], z = o_s[r][c4 + 2], w = o_s[r][c4 + 3];
-        if (out_dtype == LCS_F32) *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(x, y, z, w);
-        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
-    }
 }
 
 bool use_tc(const AttendKv4Args& a) { return a.q_dtype == LCS_BF16 && a.d_c == kDv && a.d_r == kD - kDv; }
@@ -1022,6 +1023,39 @@ int kv4_splits(const AttendKv4Args& a) {
     return best;
 }
 
+// Whether the launch's clusters of `splits` CTAs can all be resident at once (asked once per device and
+// split count; clusters of more than 8 are not portable, but open on this device).
+bool kv4_cluster_ok(int splits, int64_t units) {
+    if (splits < 2 || splits > kMaxCluster) return false;
+    constexpr int kDevices = 16;
+    static std::mutex mu;
+    static int cache[kDevices][kMaxCluster + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (cache[dev][splits] == 0) {
+        int n = 0;
+        if (set_smem_here(reinterpret_cast<const void*>(attend_kv4_tc_kernel), kTcSmem) == cudaSuccess &&
+            cudaFuncSetAttribute(attend_kv4_tc_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)splits);
+            cfg.blockDim = dim3(kTcThreads);
+            cfg.dynamicSmemBytes = kTcSmem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)splits;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, attend_kv4_tc_kernel, &cfg) != cudaSuccess) n = 0;
+        }
+        cudaGetLastError();
+        cache[dev][splits] = n > 0 ? n : -1;
+    }
+    return cache[dev][splits] >= units;
+}
+
 cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaStream_t s) {
     const int tiles = (a.H + kH - 1) / kH;
     const int64_t units = a.B * a.Q * tiles;
@@ -1034,11 +1068,25 @@ cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaSt
         part_o = static_cast<float*>(scratch);
         part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + align256(units * splits * kH * kDv * 4));
     }
-    e = launch_k(attend_kv4_tc_kernel, splits > 1 ? dim3((unsigned)splits, (unsigned)units) : dim3((unsigned)units),
-                 dim3(kTcThreads), kTcSmem, s, true, a, tiles, splits, part_o, part_ml, status);
-    if (e != cudaSuccess || splits == 1) return e;
-    return launch_k(kv4_merge_kernel, dim3((unsigned)(units * 32)), dim3(kMergeThreads), 0, s, true, part_o, part_ml,
-                    splits, a.H, tiles, a.out, a.out_dtype, a.lse);
+    const int clustered = kv4_cluster_ok(splits, units) ? 1 : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = splits > 1 ? dim3((unsigned)splits, (unsigned)units) : dim3((unsigned)units);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = kTcSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1 + clustered;
+    e = cudaLaunchKernelEx(&cfg, attend_kv4_tc_kernel, a, tiles, splits, clustered, part_o, part_ml, status);
+    if (e != cudaSuccess || splits == 1 || clustered) return e;
+    return launch_k(kv4_merge_kernel, dim3((unsigned)(units * 32)), dim3(kMergeThreads), 0, s, true, a, tiles, splits,
+                    part_o, part_ml);
 }
 
 }  // namespace
