@@ -641,9 +641,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return v < kChunk ? v : kChunk;
     };
     const bool only = splits == 1;
-#if defined(__CUDA_ARCH__)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the split merge: it may come in and wait
-#endif
 
     if (warp == kWarpQK) {
         // ---------------- Q.K^T issue
@@ -978,6 +975,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         else
             for (int t = t0; t < 256; t += dt) merge_task<1, 8>(a, tiles, splits, unit, t, part_o, part_ml);
     }
+#if defined(__CUDA_ARCH__)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the split merge
+#endif
     if (warp == kWarpQK) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -986,6 +986,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // Merges the split partials of a launch whose splits are no clusters: a warp per task.
 constexpr int kMergeThreads = 256;
+template <int S>
 __global__ void __launch_bounds__(kMergeThreads)
     kv4_merge_kernel(const AttendKv4Args a, int tiles, int splits, const float* __restrict__ part_o,
                      const float* __restrict__ part_ml) {
@@ -993,7 +994,7 @@ __global__ void __launch_bounds__(kMergeThreads)
 #if defined(__CUDA_ARCH__)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 #endif
-    merge_task<1, 16>(a, tiles, splits, w >> 8, w & 255, part_o, part_ml);
+    merge_task<1, S>(a, tiles, splits, w >> 8, w & 255, part_o, part_ml);
 #if defined(__CUDA_ARCH__)
     // the partials are read: the next kernel of the stream may be set up
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1002,19 +1003,21 @@ __global__ void __launch_bounds__(kMergeThreads)
 
 bool use_tc(const AttendKv4Args& a) { return a.q_dtype == LCS_BF16 && a.d_c == kDv && a.d_r == kD - kDv; }
 
-// Splits per (query, head tile): every CTA resident at once (one per SM), at least two chunks a
-// split; the count that minimises the longest split's chunks plus a fixed cost of about two chunks
-// (prologue, fill, epilogue) and, with splits, of the merge, which grows with their number.
+// Splits per (query, head tile): every CTA resident at once (one per SM); the count that minimises the
+// longest split's chunks plus the merge, both in chunk times (about 1.1 us).  Measured, us a call by
+// splits: 4 chunks of one query 14.1 (1), 16.1 (2); 14 chunks of 32 queries 25.9 (2), 23.4 (3), 20.4
+// (4); 25 of 4: 20.6 (8), 17.7 (9), 16.4 (13); 177 of one 26.7 (16), 22.1 (29), 20.8 (58); 177 of
+// 16: 40.2 (8, clusters), 39.4 (9, merged by a kernel).
 int kv4_splits(const AttendKv4Args& a) {
     const int64_t units = a.B * a.Q * ((a.H + kH - 1) / kH);
     const int64_t most_w = a.q_pos == nullptr ? a.Tw : (a.W < a.Tw ? a.W : a.Tw);
     const int64_t chunks = (most_w + kChunk - 1) / kChunk +
                            ((a.idx != nullptr ? a.k : a.max_blocks * a.be) + kChunk - 1) / kChunk;
     int best = 1;
-    double best_cost = (double)chunks + 2.0;
-    for (int s = 2; s <= kMaxSplits; ++s) {
-        if ((chunks + s - 1) / s < 2 || units * s > num_sms()) break;
-        const double cost = (double)((chunks + s - 1) / s) + 3.0 + s / 16.0;
+    double best_cost = (double)chunks;
+    for (int s = 2; s <= kMaxSplits && s <= chunks && units * s <= num_sms(); ++s) {
+        const bool cluster = s <= 8 || (s == kMaxCluster && units * s <= num_sms() / 2);
+        const double cost = (double)((chunks + s - 1) / s) + (cluster ? 3.5 : 4.5 + s / 32.0);
         if (cost < best_cost) {
             best = s;
             best_cost = cost;
@@ -1085,7 +1088,8 @@ cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaSt
     cfg.numAttrs = 1 + clustered;
     e = cudaLaunchKernelEx(&cfg, attend_kv4_tc_kernel, a, tiles, splits, clustered, part_o, part_ml, status);
     if (e != cudaSuccess || splits == 1 || clustered) return e;
-    return launch_k(kv4_merge_kernel, dim3((unsigned)(units * 32)), dim3(kMergeThreads), 0, s, true, a, tiles, splits,
+    // (44 splits of one query: 16 in flight 21.3 us a call, 8 22.8; 9 splits of 16: 40.7 and 39.4)
+    return launch_k(splits > 16 ? kv4_merge_kernel<16> : kv4_merge_kernel<8>, dim3((unsigned)(units * 32)), dim3(kMergeThreads), 0, s, true, a, tiles, splits,
                     part_o, part_ml);
 }
 
