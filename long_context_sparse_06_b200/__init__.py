@@ -369,23 +369,53 @@ def kv_fp4_row_bytes(d_c=512, d_r=64):
     return (d_c // 2 + 2 * d_r + d_c // 32 + 15) // 16 * 16
 
 
-def _need(t, name, dtype, shape=None, like=None):
-    """Checks one argument of a paged-cache call (the C call sees addresses only)."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {shape} expected, got {tuple(t.shape)}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, the other tensors on {like.device}")
+# These calls last about as long as the GPU needs for one of them in a decode step, so their bindings do
+# little else than check the arguments: one test per tensor, the raw stream handle, one allocation.
+def _arg(t, name, dtype, shape, dev):
+    """The address of tensor `t` (the C call sees addresses only), or ValueError."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev} expected, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
+    return t.data_ptr()
 
 
-def _call_on(t, name, stream, *args):
-    """The call on t's device: with that device current, on `stream` or its current stream."""
+def _dev(t):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("liblcs takes CUDA tensors only")
+    return dev
+
+
+_fns = {}
+
+
+def _call_on(dev, name, stream, *args):
+    """The call on device `dev`: with it current, on `stream` or its current stream."""
     torch = _torch()
-    if t.device.index == torch.cuda.current_device():
-        return _call(name, *args, _stream(stream))
-    with torch.cuda.device(t.device):
-        return _call(name, *args, _stream(stream))
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc != 0:
+        raise LcsError(name, rc)
+
+
+def _ws(ws, nbytes, dev):
+    """(address, bytes) of the workspace given, or of a new one of nbytes()."""
+    if ws is None:
+        ws = workspace(nbytes(), f"cuda:{dev}")
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous tensor on cuda:{dev} expected")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _status_bytes():
+    return 256
 
 
 def lcs_page_plan(lens, n_new, free_blocks, block_table, block_tokens=128, m=4, max_slots=0, m2=0, max_slots2=0,
@@ -394,96 +424,86 @@ def lcs_page_plan(lens, n_new, free_blocks, block_table, block_tokens=128, m=4, 
     place -> (slots [max_slots], offsets [B+1], slots2 [max_slots2], offsets2 [B+1], taken [1]), int64;
     slots2 and offsets2 are None when m2 is 0."""
     torch = _torch()
-    i64 = torch.int64
-    B = lens.shape[0]
-    _need(lens, "lens", i64, (B,))
-    _need(n_new, "n_new", i64, (B,), lens)
-    _need(free_blocks, "free_blocks", torch.int32, (free_blocks.numel(),), lens)
-    _need(block_table, "block_table", torch.int32, (B, block_table.shape[-1]), lens)
-    dev = lens.device
-    slots = torch.empty(max_slots, dtype=i64, device=dev)
-    off = torch.empty(B + 1, dtype=i64, device=dev)
-    slots2 = torch.empty(max_slots2, dtype=i64, device=dev) if m2 else None
-    off2 = torch.empty(B + 1, dtype=i64, device=dev) if m2 else None
-    taken = torch.empty(1, dtype=i64, device=dev)
-    if ws is None:
-        ws = workspace(256, dev)
-    _call_on(lens, "lcs_page_plan", stream, B, _ptr(lens), _ptr(n_new), block_tokens, _ptr(free_blocks),
-             free_blocks.numel(), _ptr(block_table), block_table.shape[1], m, _ptr(slots), max_slots, _ptr(off), m2,
-             _ptr(slots2), max_slots2 if m2 else 0, _ptr(off2), _ptr(taken), _ptr(ws), ws.numel())
-    return slots, off, slots2, off2, taken
+    i64, i32 = torch.int64, torch.int32
+    dev = _dev(lens)
+    B, n_free, max_blocks = lens.shape[0], free_blocks.numel(), block_table.shape[-1]
+    head = (B, _arg(lens, "lens", i64, (B,), dev), _arg(n_new, "n_new", i64, (B,), dev), block_tokens,
+            _arg(free_blocks, "free_blocks", i32, (n_free,), dev), n_free,
+            _arg(block_table, "block_table", i32, (B, max_blocks), dev), max_blocks)
+    wp, wb, ws = _ws(ws, _status_bytes, dev)
+    if m2:
+        out = lens.new_empty(max_slots + max_slots2 + 2 * B + 3)
+        slots, slots2, off, off2, taken = out.split_with_sizes((max_slots, max_slots2, B + 1, B + 1, 1))
+        p = out.data_ptr()
+        p2 = p + 8 * max_slots
+        po = p2 + 8 * max_slots2
+        _call_on(dev, "lcs_page_plan", stream, *head, m, p, max_slots, po, m2, p2, max_slots2, po + 8 * (B + 1),
+                 po + 16 * (B + 1), wp, wb)
+        return slots, off, slots2, off2, taken
+    out = lens.new_empty(max_slots + B + 2)
+    slots, off, taken = out.split_with_sizes((max_slots, B + 1, 1))
+    p = out.data_ptr()
+    po = p + 8 * max_slots
+    _call_on(dev, "lcs_page_plan", stream, *head, m, p, max_slots, po, 0, None, 0, None, po + 8 * (B + 1), wp, wb)
+    return slots, off, None, None, taken
 
 
-def _pool_slots(pool, d_c, d_r, like):
-    """Slots of a pool [n_blocks, block_entries, row] (or [n_slots, row]) of 4-bit rows."""
-    _need(pool, "pool", _torch().uint8, tuple(pool.shape[:-1]) + (kv_fp4_row_bytes(d_c, d_r),), like)
-    n = 1
-    for s in pool.shape[:-1]:
-        n *= s
-    return n
+def _pool_arg(pool, d_c, d_r, dev):
+    """(address, slots) of a pool [n_blocks, block_entries, row] (or [n_slots, row]) of 4-bit rows."""
+    rb = kv_fp4_row_bytes(d_c, d_r)
+    return _arg(pool, "pool", _torch().uint8, pool.shape[:-1] + (rb,), dev), pool.numel() // rb
 
 
 def lcs_kv4_store(x, slots, pool, d_c=512, ws=None, stream=None):
     """Quantises x [n, d_c + d_r] (fp32/bf16) into the pool's 4-bit rows at slots [n] int64 (negative: skipped)."""
+    dev = _dev(x)
     n, D = x.shape
-    _need(slots, "slots", _torch().int64, (n,), x)
-    n_slots = _pool_slots(pool, d_c, D - d_c, x)
-    if ws is None:
-        ws = workspace(256, x.device)
-    _call_on(x, "lcs_kv4_store", stream, _ptr(x), _dt(x), n, d_c, D - d_c, _ptr(slots), _ptr(pool), n_slots, _ptr(ws),
-             ws.numel())
+    pp, n_slots = _pool_arg(pool, d_c, D - d_c, dev)
+    wp, wb, ws = _ws(ws, _status_bytes, dev)
+    _call_on(dev, "lcs_kv4_store", stream, _arg(x, "x", x.dtype, (n, D), dev), _dt(x), n, d_c, D - d_c,
+             _arg(slots, "slots", _torch().int64, (n,), dev), pp, n_slots, wp, wb)
     return pool
 
 
 def lcs_kv4_load(pool, slots, d_c=512, d_r=64, out_dtype=None, out=None, ws=None, stream=None):
     """The values of the pool's rows at slots [n] int64 (negative: zeros) -> [n, d_c + d_r] (bf16 or fp32)."""
     torch = _torch()
-    _need(slots, "slots", torch.int64, (slots.numel(),), pool)
-    n_slots = _pool_slots(pool, d_c, d_r, pool)
-    n = slots.shape[0]
+    dev = _dev(pool)
+    n = slots.numel()
+    pp, n_slots = _pool_arg(pool, d_c, d_r, dev)
     if out is None:
-        out = torch.empty((n, d_c + d_r), dtype=out_dtype or torch.bfloat16, device=pool.device)
-    else:
-        _need(out, "out", out_dtype or out.dtype, (n, d_c + d_r), pool)
-    if ws is None:
-        ws = workspace(256, pool.device)
-    _call_on(pool, "lcs_kv4_load", stream, _ptr(pool), n_slots, _ptr(slots), n, d_c, d_r, _ptr(out), _dt(out), _ptr(ws),
-             ws.numel())
+        out = pool.new_empty((n, d_c + d_r), dtype=out_dtype or torch.bfloat16)
+    wp, wb, ws = _ws(ws, _status_bytes, dev)
+    _call_on(dev, "lcs_kv4_load", stream, pp, n_slots, _arg(slots, "slots", torch.int64, (n,), dev), n, d_c, d_r,
+             _arg(out, "out", out_dtype or out.dtype, (n, d_c + d_r), dev), _dt(out), wp, wb)
     return out
 
 
 def _attend_kv4(name, q, pool, block_table, n_entries, win, idx, k, hca_m, scale, d_c, n_win, q_pos, win_pos0, W,
                 want_lse, out_dtype, ws, stream):
     torch = _torch()
+    i64, dt, dev = torch.int64, q.dtype, _dev(q)
     B, Q, H, D = q.shape
-    _need(pool, "pool", torch.uint8, tuple(pool.shape[:2]) + (kv_fp4_row_bytes(d_c, D - d_c),), q)
-    n_blocks, be, _ = pool.shape
-    max_blocks = block_table.shape[1]
-    _need(block_table, "block_table", torch.int32, (B, max_blocks), q)
-    _need(n_entries, "n_entries", torch.int64, (B,), q)
-    Tw = 0
-    if win is not None:
-        Tw = win.shape[1]
-        _need(win, "win", q.dtype, (B, Tw, D), q)
-    if n_win is not None:
-        _need(n_win, "n_win", torch.int64, (B,), q)
-    if q_pos is not None:
-        _need(q_pos, "q_pos", torch.int64, (B, Q), q)
-    if win_pos0 is not None:
-        _need(win_pos0, "win_pos0", torch.int64, (B,), q)
-    if idx is not None:
-        _need(idx, "idx", torch.int32, (B, Q, k), q)
-    out = torch.empty((B, Q, H, d_c), dtype=out_dtype or q.dtype, device=q.device)
-    lse = torch.empty((B, Q, H), dtype=torch.float32, device=q.device) if want_lse else None
-    if ws is None:
-        ws = workspace(lcs_workspace_size(OP_ATTEND_KV4, B, Q, max_blocks * be, Tw, k, H, d_c), q.device)
-    tail = (W, H, d_c, D - d_c, scale, _ptr(out), _dt(out), _ptr(lse), _ptr(ws), ws.numel())
-    head = (_ptr(q), _dt(q), _ptr(pool), n_blocks, be, _ptr(block_table), max_blocks, _ptr(n_entries), _ptr(win),
-            _ptr(n_win), B, Q, Tw)
+    n_blocks, be, rb = pool.shape
+    max_blocks = block_table.shape[-1]
+    Tw = 0 if win is None else win.shape[1]
+    out = q.new_empty((B, Q, H, d_c), dtype=out_dtype or dt)
+    lse = q.new_empty((B, Q, H), dtype=torch.float32) if want_lse else None
+    wp, wb, ws = _ws(ws, lambda: lcs_workspace_size(OP_ATTEND_KV4, B, Q, max_blocks * be, Tw, k, H, d_c), dev)
+    bf16 = torch.bfloat16
+    head = (_arg(q, "q", dt, (B, Q, H, D), dev), BF16 if dt is bf16 else _dt(q),
+            _arg(pool, "pool", torch.uint8, (n_blocks, be, kv_fp4_row_bytes(d_c, D - d_c)), dev), n_blocks, be,
+            _arg(block_table, "block_table", torch.int32, (B, max_blocks), dev), max_blocks,
+            _arg(n_entries, "n_entries", i64, (B,), dev), None if win is None else _arg(win, "win", dt, (B, Tw, D), dev),
+            None if n_win is None else _arg(n_win, "n_win", i64, (B,), dev), B, Q, Tw)
+    tail = (None if q_pos is None else _arg(q_pos, "q_pos", i64, (B, Q), dev),
+            None if win_pos0 is None else _arg(win_pos0, "win_pos0", i64, (B,), dev),
+            *(() if hca_m is None else (hca_m,)), W, H, d_c, D - d_c, scale, out.data_ptr(), BF16 if out.dtype is bf16 else _dt(out),
+            None if lse is None else lse.data_ptr(), wp, wb)
     if hca_m is None:
-        _call_on(q, name, stream, *head, _ptr(idx), k, _ptr(q_pos), _ptr(win_pos0), *tail)
+        _call_on(dev, name, stream, *head, _arg(idx, "idx", torch.int32, (B, Q, k), dev), k, *tail)
     else:
-        _call_on(q, name, stream, *head, _ptr(q_pos), _ptr(win_pos0), hca_m, *tail)
+        _call_on(dev, name, stream, *head, *tail)
     return (out, lse) if want_lse else out
 
 

@@ -66,32 +66,41 @@ __device__ __forceinline__ const uint8_t* kv4_row(const AttendKv4Args& a, int64_
 
 // ------------------------------------------------------------ CUDA-core path
 // Every shape: H <= 128, d_c % 32 == 0 and <= 512, d_r <= 128, fp32 or bf16 queries.  One CTA per
-// query and group of 8 heads: 32 rows at a time widened to fp32 in shared memory, the scores
-// by one thread per (head, row), an online softmax by one warp per head, the outputs in
-// registers.  Bound by shared-memory reads (two per multiply-add); it serves the small shapes.
-constexpr int kSThreads = 256, kSRows = 32, kSHeads = 8;
+// query and group of 8 heads: 64 rows at a time widened to fp32 in shared memory; a warp per head
+// forms the scores of two rows a lane (16-byte reads: a row's pitch of D + 4 floats puts a quarter
+// warp's eight rows on different banks) and runs the online softmax; for the outputs a thread
+// holds 4 dims of a head, and threads left over share the rows (summed at the end).  Bound by
+// latency: the rows' addresses are fetched one step ahead.  It serves the small shapes: 1024 causal
+// queries of 8 heads, D = 80, up to 192 rows each.
+constexpr int kSThreads = 256, kSRows = 64, kSHeads = 8;
 constexpr int kSMaxDc = 512;
-constexpr int kSAcc = kSHeads * kSMaxDc / kSThreads;
 
 __device__ __forceinline__ float ld_elem(const void* p, int64_t i, int dtype) {
     return dtype == LCS_F32 ? static_cast<const float*>(p)[i]
                             : bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
+__device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
+    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
+}
 
+// kItems: output pieces (4 dims of a head) per thread, at least 8 d_c / 4 / 256.
+template <int kItems>
 __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Args a, int* status) {
-    extern __shared__ float sh[];
-    const int D = a.d_c + a.d_r, pitch = D + 1;
-    float* qs = sh;                          // [heads, D]
-    float* rows = qs + kSHeads * D;          // [32, D + 1]
-    float* sc = rows + kSRows * pitch;       // [heads, 33]
-    float* al = sc + kSHeads * (kSRows + 1); // [heads] rescale of this chunk
-    float* lh = al + kSHeads;                // [heads] sums
+    extern __shared__ float4 sh4[];
+    float* sh = reinterpret_cast<float*>(sh4);
+    const int D = a.d_c + a.d_r, pitch = D + 4;
+    float* qs = sh;                            // [heads, D]
+    float* rows = qs + kSHeads * D;            // [64, D + 4]
+    float* sc = rows + kSRows * pitch;         // [heads, 64] weights of this chunk
+    __shared__ float al[kSHeads], lh[kSHeads];
+    __shared__ const uint8_t* ptr[2][kSRows];
     __shared__ int nsel_s;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int64_t g = blockIdx.x, b = g / a.Q;
     const int h0 = blockIdx.y * kSHeads, nh = min(kSHeads, a.H - h0);
 
-    for (int i = t; i < nh * D; i += kSThreads) qs[i] = ld_elem(a.q, (g * a.H + h0) * D + i, a.q_dtype);
+    for (int i = t; i < kSHeads * D; i += kSThreads)
+        qs[i] = i < nh * D ? ld_elem(a.q, (g * a.H + h0) * D + i, a.q_dtype) : 0.f;
     const int64_t n = kv4_entries(a, b, status);
     const int32_t* sel = a.idx != nullptr ? a.idx + g * a.k : nullptr;
     if (t == 0) nsel_s = sel != nullptr ? a.k : (int)kv4_avail(a, g, n);
@@ -102,73 +111,106 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
             if (v < 0 || v >= n) atomicMin(&nsel_s, i);
         }
     __syncthreads();
-    const int64_t nsel = nsel_s;
+    const int nsel = nsel_s;
     if (sel != nullptr && t == 0 && nsel < a.k && sel[nsel] >= 0) set_status(status, LCS_ERR_DEVICE, 603);
     const Kv4Window win = kv4_window(a, g, b);
-    const int64_t R = nsel + win.n;
+    const int R = nsel + (int)win.n;
+    // address of list row r: a compressed row (null if its block is not one of the pool's) or a window row
+    auto row_at = [&](int r) -> const uint8_t* {
+        if (r >= R) return nullptr;
+        if (r >= nsel)
+            return static_cast<const uint8_t*>(a.win) + (b * a.Tw + win.lo + (r - nsel)) * D * (a.q_dtype == LCS_F32 ? 4 : 2);
+        const uint8_t* p = kv4_row(a, b, sel != nullptr ? __ldg(sel + r) : r);
+        if (p == nullptr) set_status(status, LCS_ERR_DEVICE, 602);
+        return p;
+    };
+    if (t < kSRows) ptr[0][t] = row_at(t);
 
-    float acc[kSAcc];
+    // outputs: item j = (head, 4 dims) of nh d_c / 4; `share` threads split an item's rows
+    const int c4n = a.d_c / 4, items = nh * c4n;
+    int share = 1;
+    while (share < 32 && items * share * 2 <= kSThreads) share *= 2;
+    const int part = t % share, first = t / share, step = kSThreads / share;
+    float4 acc[kItems];
 #pragma unroll
-    for (int i = 0; i < kSAcc; ++i) acc[i] = 0.f;
-    float m = -INFINITY, l = 0.f;            // of head `warp`, the same in every lane
-    const int blocks = a.d_c / 32;
-    for (int64_t r0 = 0; r0 < R; r0 += kSRows) {
-        const int nr = (int)(R - r0 < kSRows ? R - r0 : kSRows);
-        const int nc = (int)(nsel - r0 < 0 ? 0 : (nsel - r0 < nr ? nsel - r0 : nr));   // compressed rows among them
-        for (int i = t; i < nc * blocks; i += kSThreads) {
-            const int r = i / blocks, bl = i - r * blocks;
-            const uint8_t* src = kv4_row(a, b, sel != nullptr ? sel[r0 + r] : (int)(r0 + r));
-            if (src == nullptr) set_status(status, LCS_ERR_DEVICE, 602);
-            float* o = rows + r * pitch + 32 * bl;
-            const uint4 c = src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src) + bl) : make_uint4(0, 0, 0, 0);
-            const float s = src != nullptr ? e4m3_to_f32(src[a.d_c / 2 + 2 * a.d_r + bl]) : 0.f;
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    for (int i = 0; i < kItems; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;              // of head `warp`, the same in every lane
+    __syncthreads();
+    for (int r0 = 0, k = 0; r0 < R; r0 += kSRows, k ^= 1) {
+        const int nr = min(kSRows, R - r0), nc = max(0, min(nr, nsel - r0));   // rows, compressed ones among them
+        if (t < kSRows) ptr[k ^ 1][t] = row_at(r0 + kSRows + t);
+        const int c16 = a.d_c / 16;
+        for (int i = t; i < nc * c16; i += kSThreads) {
+            const int r = i / c16, c = i - r * c16;
+            const uint8_t* src = ptr[k][r];
+            float4* o = reinterpret_cast<float4*>(rows + r * pitch + 16 * c);
+            const uint2 w = src != nullptr ? __ldg(reinterpret_cast<const uint2*>(src) + c) : make_uint2(0, 0);
+            const float s = src != nullptr ? e4m3_to_f32(__ldg(src + a.d_c / 2 + 2 * a.d_r + c / 2)) : 0.f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float2 f = e2m1x2_to_f32(w[k >> 2] >> (8 * (k & 3)));
-                o[2 * k] = f.x * s;
-                o[2 * k + 1] = f.y * s;
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t x = (q < 2 ? w.x : w.y) >> (16 * (q & 1));
+                const float2 u = e2m1x2_to_f32(x), v = e2m1x2_to_f32(x >> 8);
+                o[q] = make_float4(u.x * s, u.y * s, v.x * s, v.y * s);
             }
         }
-        for (int i = t; i < nc * a.d_r; i += kSThreads) {
-            const int r = i / a.d_r, j = i - r * a.d_r;
-            const uint8_t* src = kv4_row(a, b, sel != nullptr ? sel[r0 + r] : (int)(r0 + r));
-            rows[r * pitch + a.d_c + j] =
-                src != nullptr ? bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(src + a.d_c / 2 + 2 * j)) : 0.f;
+        for (int i = t; i < nc * a.d_r / 2; i += kSThreads) {
+            const int r = i / (a.d_r / 2), j = 2 * (i - r * (a.d_r / 2));
+            const uint8_t* src = ptr[k][r];
+            const uint32_t w = src != nullptr ? __ldg(reinterpret_cast<const uint32_t*>(src + a.d_c / 2 + 2 * j)) : 0u;
+            *reinterpret_cast<float2*>(rows + r * pitch + a.d_c + j) = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
         }
-        for (int i = t; i < (nr - nc) * D; i += kSThreads) {
-            const int r = i / D, j = i - r * D;
-            rows[(nc + r) * pitch + j] = ld_elem(a.win, (b * a.Tw + win.lo + (r0 + nc + r - nsel)) * D + j, a.q_dtype);
+        for (int i = t; i < (nr - nc) * (D / 4); i += kSThreads) {
+            const int r = nc + i / (D / 4), j = 4 * (i % (D / 4));
+            float4 v;
+            if (a.q_dtype == LCS_F32) v = __ldg(reinterpret_cast<const float4*>(ptr[k][r]) + j / 4);
+            else {
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(ptr[k][r]) + j / 4);
+                v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                                __uint_as_float(w.y & 0xFFFF0000u));
+            }
+            *reinterpret_cast<float4*>(rows + r * pitch + j) = v;
         }
         __syncthreads();
-        {   // thread = (head, row): a warp's lanes take the 32 rows of one head
-            float s = -INFINITY;
-            if (warp < nh && lane < nr) {
-                const float* qh = qs + warp * D;
-                const float* rr = rows + lane * pitch;
-                s = 0.f;
-                for (int c = 0; c < D; ++c) s = fmaf(qh[c], rr[c], s);
-                s *= a.scale;
-            }
-            const float mx = fmaxf(m, warp_max(s));
-            const float alpha = m == -INFINITY ? 0.f : expf(m - mx);
-            const float p = s == -INFINITY ? 0.f : expf(s - mx);
-            l = l * alpha + warp_sum(p);
-            m = mx;
+        {   // warp = head, lane = rows lane and lane + 32
+            float s[2] = {-INFINITY, -INFINITY};
             if (warp < nh) {
-                sc[warp * (kSRows + 1) + lane] = p;
-                if (lane == 0) al[warp] = alpha;
+                const float4* q4 = reinterpret_cast<const float4*>(qs + warp * D);
+                const float4* ra = reinterpret_cast<const float4*>(rows + lane * pitch);
+                const float4* rb = reinterpret_cast<const float4*>(rows + (lane + 32) * pitch);
+                float sa = 0.f, sb = 0.f;   // (rows past nr hold anything: dropped below)
+#pragma unroll 4
+                for (int c = 0; c < D / 4; ++c) {
+                    const float4 q = q4[c];
+                    sa = dot4(q, ra[c], sa);
+                    if (nr > 32) sb = dot4(q, rb[c], sb);
+                }
+                if (lane < nr) s[0] = sa * a.scale;
+                if (lane + 32 < nr) s[1] = sb * a.scale;
             }
+            const float mx = fmaxf(m, warp_max(fmaxf(s[0], s[1])));
+            const float alpha = m == -INFINITY ? 0.f : expf(m - mx);
+            const float p0 = s[0] == -INFINITY ? 0.f : expf(s[0] - mx), p1 = s[1] == -INFINITY ? 0.f : expf(s[1] - mx);
+            l = l * alpha + warp_sum(p0 + p1);
+            m = mx;
+            sc[warp * kSRows + lane] = p0;
+            sc[warp * kSRows + 32 + lane] = p1;
+            if (lane == 0) al[warp] = alpha;
         }
         __syncthreads();
-        // thread = (head, output dim): 16 per thread at most
 #pragma unroll
-        for (int i = 0; i < kSAcc; ++i) {
-            const int j = t + kSThreads * i;
-            if (j >= nh * a.d_c) break;
-            const int h = j / a.d_c, c = j - h * a.d_c;
-            float o = acc[i] * al[h];
-            for (int r = 0; r < nr; ++r) o = fmaf(sc[h * (kSRows + 1) + r], rows[r * pitch + c], o);
+        for (int i = 0; i < kItems; ++i) {
+            const int j = first + step * i;
+            if (j >= items) break;
+            const int h = j / c4n, c = j - h * c4n;
+            const float f = al[h];
+            float4 o = make_float4(acc[i].x * f, acc[i].y * f, acc[i].z * f, acc[i].w * f);
+            const float4* v4 = reinterpret_cast<const float4*>(rows + 4 * c);
+#pragma unroll 4
+            for (int r = part; r < nr; r += share) {
+                const float p = sc[h * kSRows + r];
+                const float4 v = v4[r * (pitch / 4)];
+                o = make_float4(fmaf(p, v.x, o.x), fmaf(p, v.y, o.y), fmaf(p, v.z, o.z), fmaf(p, v.w, o.w));
+            }
             acc[i] = o;
         }
         __syncthreads();
@@ -179,14 +221,24 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kSAcc; ++i) {
-        const int j = t + kSThreads * i;
-        if (j >= nh * a.d_c) break;
-        const int h = j / a.d_c;
-        const float o = lh[h] > 0.f ? acc[i] / lh[h] : 0.f;
-        const int64_t at = (g * a.H + h0) * a.d_c + j;
-        if (a.out_dtype == LCS_F32) static_cast<float*>(a.out)[at] = o;
-        else static_cast<uint16_t*>(a.out)[at] = f32_to_bf16_bits(o);
+    for (int i = 0; i < kItems; ++i) {
+        const int j = first + step * i;
+        float4 o = acc[i];
+        for (int d = 1; d < share; d <<= 1) {   // the threads that shared an item are neighbours in a warp
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, d);
+            o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
+            o.z += __shfl_xor_sync(0xffffffffu, o.z, d);
+            o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+        }
+        if (j >= items || part != 0) continue;
+        const int h = j / c4n;
+        const float iv = lh[h] > 0.f ? 1.f / lh[h] : 0.f;
+        const int64_t at = (g * a.H + h0) * a.d_c + 4 * j;
+        if (a.out_dtype == LCS_F32)
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+                make_uint2(pack_bf16x2(o.x * iv, o.y * iv), pack_bf16x2(o.z * iv, o.w * iv));
     }
 }
 
@@ -1109,11 +1161,12 @@ cudaError_t launch_attend_kv4(const AttendKv4Args& a, void* scratch, int* status
     if (queries == 0) return cudaSuccess;
     if (use_tc(a)) return launch_tc(a, scratch, status, s);
     const int D = a.d_c + a.d_r;
-    const size_t smem = sizeof(float) * (kSHeads * D + kSRows * (D + 1) + kSHeads * (kSRows + 1) + 2 * kSHeads);
-    cudaError_t e = set_smem_here(reinterpret_cast<const void*>(attend_kv4_kernel), smem);
+    const size_t smem = sizeof(float) * (kSHeads * D + kSRows * (D + 4) + kSHeads * kSRows);
+    auto kern = a.d_c <= 128 ? attend_kv4_kernel<kSHeads * 128 / 4 / kSThreads> : attend_kv4_kernel<kSHeads * kSMaxDc / 4 / kSThreads>;
+    cudaError_t e = set_smem_here(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
-    return launch_k(attend_kv4_kernel, dim3((unsigned)queries, (unsigned)((a.H + kSHeads - 1) / kSHeads)),
-                    dim3(kSThreads), smem, s, false, a, status);
+    return launch_k(kern, dim3((unsigned)queries, (unsigned)((a.H + kSHeads - 1) / kSHeads)), dim3(kSThreads), smem, s, false,
+                    a, status);
 }
 
 }  // namespace lcs
