@@ -286,6 +286,7 @@ constexpr int kQBytes = (9 - kTQ / 64) * kQBlk;
 constexpr int kSoftWarps = 4, kProdWarps = 6, kProdGroups = 2;
 constexpr int kWarpQK = kSoftWarps + kProdGroups * kProdWarps, kWarpPV = kWarpQK + 1, kTcWarps = kWarpPV + 1;
 constexpr int kTcThreads = kTcWarps * 32;
+constexpr int kQWarps = kTcWarps - kProdWarps;                // warps that bring in Q
 constexpr int kRowsPerWarp = kChunk / kProdWarps;             // rows of a chunk per producer warp
 constexpr int kPieces = 32 / kRowsPerWarp;                    // lanes that share a row
 static_assert(kRowsPerWarp == 8, "a store's eight lanes hold eight rows: eight bank groups");
@@ -582,16 +583,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_alloc(&bars.tmem_base, 512);
         tmem_relinquish();
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)uni((int)bars.tmem_base);
 #if defined(__CUDA_ARCH__)
     asm volatile("griddepcontrol.wait;" ::: "memory");   // everything above reads no memory of the call
 #endif
     // column block k of Q: the first ones pass through the last stage into TMEM
     auto q_block = [&](int k) { return k < kTQ / 64 ? stage_s + (kStages - 1) * kStageBytes + k * kQBlk : q_s + (k - kTQ / 64) * kQBlk; };
     // ---- the loads that nothing waits for, before everything else: Q as it is, in the SW128 layout ...
-    {
+    // (by every warp but the first group of producers, which fills the first chunk meanwhile)
+    const bool q_warp = !producer || pg != 0;
+    const int q_id = warp < kSoftWarps ? warp : warp - kProdWarps;   // 0 .. kQWarps - 1
+    if (q_warp) {
         const uint8_t* qg = static_cast<const uint8_t*>(a.q) + ((int64_t)g * a.H + h0) * (kD * 2);
 #pragma unroll 4
-        for (int i = threadIdx.x; i < kH * 72; i += kTcThreads) {
+        for (int i = q_id * 32 + lane; i < kH * 72; i += kQWarps * 32) {
             const int h = i / 72, c = i - h * 72;
             cp_async_16(q_block(c >> 3) + sw128_off(h, c & 7), qg + (h < nh ? i * 16 : 0), h < nh);
         }
@@ -640,48 +648,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         first_bad = __reduce_min_sync(0xffffffffu, first_bad);
         if (lane == 0) bars.first_bad[warp] = first_bad;
     }
-    cp_async_wait<0>();
-    __syncthreads();
-    // ---- Q scaled by 2^e (and by the sign of the scale) in place, a warp per head; content to fp16
-    const uint32_t neg = a.scale < 0.f ? 0x80008000u : 0u;
-#pragma unroll 2
-    for (int h = warp; h < kH; h += kTcWarps) {
-        const uint32_t at = sw128_off(h, lane & 7);   // chunks lane, lane + 32, lane + 64
-        uint4* x0 = reinterpret_cast<uint4*>(q_block(lane >> 3) + at);
-        uint4* x1 = reinterpret_cast<uint4*>(q_block(4 + (lane >> 3)) + at);
-        uint4* x2 = reinterpret_cast<uint4*>(q_block(8) + at);
-        const uint4 v0 = *x0, v1 = *x1, v2 = *x2;     // (four lanes read each of the last 8 chunks)
-        uint32_t m2 = bf16x2_maxabs(bf16x2_maxabs(v0.x, v0.y), bf16x2_maxabs(v0.z, v0.w));
-        m2 = bf16x2_maxabs(m2, bf16x2_maxabs(bf16x2_maxabs(v1.x, v1.y), bf16x2_maxabs(v1.z, v1.w)));
-        m2 = bf16x2_maxabs(m2, bf16x2_maxabs(bf16x2_maxabs(v2.x, v2.y), bf16x2_maxabs(v2.z, v2.w)));
-        const uint32_t mag = __reduce_max_sync(0xffffffffu, max(m2 & 0x7FFFu, (m2 >> 16) & 0x7FFFu));   // bf16 bits
-        const int ex = (int)(mag >> 7) - 127;               // of the largest element (subnormals: -127)
-        int e = mag == 0 || mag >= 0x7F80u ? 0 : 14 - ex;   // zero, infinite or NaN heads stay as they are
-        e = e > 126 ? 126 : e;
-        const uint32_t up2 = (uint32_t)(127 + e) * 0x00800080u | neg;
-        if (lane == 0) bars.qscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
-        auto half8 = [&](uint4 v) {
-            auto half2 = [&](uint32_t w) {
-                w = bf16x2_mul(w, up2);
-                return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-            };
-            return make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
-        };
-        *x0 = half8(v0);
-        *x1 = half8(v1);
-        if (lane < 8)
-            *x2 = make_uint4(bf16x2_mul(v2.x, up2), bf16x2_mul(v2.y, up2), bf16x2_mul(v2.z, up2), bf16x2_mul(v2.w, up2));
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = (uint32_t)uni((int)bars.tmem_base);
     int nsel = most;
     if (sel != nullptr) {
+        __syncthreads();
         for (int i = 0; i < kTcWarps; ++i) nsel = min(nsel, bars.first_bad[i]);
         // an index past the entries ended it; -1 is the padding
         if (threadIdx.x == 0 && nsel < a.k && __ldg(sel + nsel) >= 0) set_status(status, LCS_ERR_DEVICE, 603);
+    }
+    if (q_warp) {
+        const uint32_t neg = a.scale < 0.f ? 0x80008000u : 0u;
+        auto q_sync = []() { asm volatile("bar.sync 1, %0;" ::"n"(kQWarps * 32) : "memory"); };
+        cp_async_wait<0>();
+        q_sync();
+        // ---- Q scaled by 2^e (and by the sign of the scale) in place, a warp per head; content to fp16
+#pragma unroll 2
+        for (int h = q_id; h < kH; h += kQWarps) {
+            const uint32_t at = sw128_off(h, lane & 7);   // chunks lane, lane + 32, lane + 64
+            uint4* x0 = reinterpret_cast<uint4*>(q_block(lane >> 3) + at);
+            uint4* x1 = reinterpret_cast<uint4*>(q_block(4 + (lane >> 3)) + at);
+            uint4* x2 = reinterpret_cast<uint4*>(q_block(8) + at);
+            const uint4 v0 = *x0, v1 = *x1, v2 = *x2;     // (four lanes read each of the last 8 chunks)
+            uint32_t m2 = bf16x2_maxabs(bf16x2_maxabs(v0.x, v0.y), bf16x2_maxabs(v0.z, v0.w));
+            m2 = bf16x2_maxabs(m2, bf16x2_maxabs(bf16x2_maxabs(v1.x, v1.y), bf16x2_maxabs(v1.z, v1.w)));
+            m2 = bf16x2_maxabs(m2, bf16x2_maxabs(bf16x2_maxabs(v2.x, v2.y), bf16x2_maxabs(v2.z, v2.w)));
+            const uint32_t mag = __reduce_max_sync(0xffffffffu, max(m2 & 0x7FFFu, (m2 >> 16) & 0x7FFFu));   // bf16 bits
+            const int ex = (int)(mag >> 7) - 127;               // of the largest element (subnormals: -127)
+            int e = mag == 0 || mag >= 0x7F80u ? 0 : 14 - ex;   // zero, infinite or NaN heads stay as they are
+            e = e > 126 ? 126 : e;
+            const uint32_t up2 = (uint32_t)(127 + e) * 0x00800080u | neg;
+            if (lane == 0) bars.qscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
+            auto half8 = [&](uint4 v) {
+                auto half2 = [&](uint32_t w) {
+                    w = bf16x2_mul(w, up2);
+                    return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+                };
+                return make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+            };
+            *x0 = half8(v0);
+            *x1 = half8(v1);
+            if (lane < 8)
+                *x2 = make_uint4(bf16x2_mul(v2.x, up2), bf16x2_mul(v2.y, up2), bf16x2_mul(v2.z, up2), bf16x2_mul(v2.w, up2));
+        }
+        fence_proxy_async_smem();
+        q_sync();
     }
     // this split's chunks, and the compressed ones among them, which come first
     const int ncc_all = (nsel + kChunk - 1) / kChunk, nch_all = ncc_all + (int)((wp.n + kChunk - 1) / kChunk);
