@@ -655,6 +655,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // an index past the entries ended it; -1 is the padding
         if (threadIdx.x == 0 && nsel < a.k && __ldg(sel + nsel) >= 0) set_status(status, LCS_ERR_DEVICE, 603);
     }
+    // this split's chunks, and the compressed ones among them, which come first
+    const int ncc_all = (nsel + kChunk - 1) / kChunk, nch_all = ncc_all + (int)((wp.n + kChunk - 1) / kChunk);
+    const int nch = uni(sp < nch_all ? (nch_all - sp + splits - 1) / splits : 0);
+    const int ncc = uni(sp < ncc_all ? (ncc_all - sp + splits - 1) / splits : 0);
+    // window chunk c into its stage: bf16 rows by 16-byte cp.async, pieces my_piece + 4 k of this lane's row, zeros
+    // past the last row
+    const uint32_t wo0 = sw128_off(my_row, my_piece), wo1 = sw128_off(my_row, my_piece + kPieces);
+    auto copy_window = [&](int c, int st) {
+        uint8_t* dst = stage_s + st * kStageBytes;
+        const int r = (gcof(c) - ncc_all) * kChunk + my_row;
+        const bool valid = r < (int)wp.n;
+        const uint8_t* src = static_cast<const uint8_t*>(a.win) + (((int64_t)b * a.Tw + wp.lo + (valid ? r : 0)) * kD) * 2 + 16 * my_piece;
+#pragma unroll
+        for (int k = 0; k < 72 / kPieces; ++k)
+            cp_async_16(dst + (k >> 1) * kBlk + (k & 1 ? wo1 : wo0), src + 16 * kPieces * k, valid);
+        cp_async_commit();
+    };
+    if (producer && pg >= ncc && pg < nch) copy_window(pg, pg);
     if (q_warp) {
         const uint32_t neg = a.scale < 0.f ? 0x80008000u : 0u;
         auto q_sync = []() { asm volatile("bar.sync 1, %0;" ::"n"(kQWarps * 32) : "memory"); };
@@ -692,10 +710,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         fence_proxy_async_smem();
         q_sync();
     }
-    // this split's chunks, and the compressed ones among them, which come first
-    const int ncc_all = (nsel + kChunk - 1) / kChunk, nch_all = ncc_all + (int)((wp.n + kChunk - 1) / kChunk);
-    const int nch = uni(sp < nch_all ? (nch_all - sp + splits - 1) / splits : 0);
-    const int ncc = uni(sp < ncc_all ? (ncc_all - sp + splits - 1) / splits : 0);
     auto chunk_valid = [&](int c) -> int {   // rows of local chunk c
         const int gc = gcof(c);
         const int v = c < ncc ? nsel - gc * kChunk : (int)wp.n - (gc - ncc_all) * kChunk;
@@ -778,21 +792,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (c >= kStages && (!warp_wait(&bars.kempty[st][0], ph, status, 609) ||
                                      !warp_wait(&bars.kempty[st][1], ph, status, 610)))
                     break;
-                const int w0 = (gcof(c) - ncc_all) * kChunk;
-                const uint8_t* src = static_cast<const uint8_t*>(a.win) + ((int64_t)b * a.Tw + wp.lo + w0) * (kD * 2);
-                const uint32_t r0 = pw * kRowsPerWarp;
-#pragma unroll 2
-                for (int i = lane; i < kRowsPerWarp * 72; i += 32) {
-                    const uint32_t r = r0 + (uint32_t)i / 72u, ch = (uint32_t)i % 72u;
-                    const bool valid = w0 + (int)r < (int)wp.n;
-                    cp_async_16(dst + (ch >> 3) * kBlk + sw128_off(r, ch & 7), src + (valid ? r * (kD * 2) + ch * 16 : 0), valid);
-                }
-                cp_async_commit();
+                if (c != pg) copy_window(c, st);   // the first is on its way
                 cp_async_wait<0>();
-                __syncwarp();
 #pragma unroll 4
-                for (int i = lane; i < kRowsPerWarp * 64; i += 32) {
-                    uint4* x = reinterpret_cast<uint4*>(dst + ((i & 63) >> 3) * kBlk + sw128_off(r0 + (i >> 6), i & 7));
+                for (int k = 0; k < 64 / kPieces; ++k) {   // a lane's own copies
+                    uint4* x = reinterpret_cast<uint4*>(dst + (k >> 1) * kBlk + (k & 1 ? wo1 : wo0));
                     const uint4 v = *x;
                     *x = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
                 }
@@ -1032,7 +1036,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (splits <= 2)
             for (int t = t0; t < 64; t += dt) merge_task<4, 2>(a, tiles, splits, unit, t, part_o, part_ml);
         else if (splits <= 4)
-            for (int t = t0; t < 128; t += dt) merge_task<2, 4>(a, tiles, splits, unit, t, part_o, part_ml);
+            for (int t = t0; t < 64; t += dt) merge_task<4, 4>(a, tiles, splits, unit, t, part_o, part_ml);
         else
             for (int t = t0; t < 256; t += dt) merge_task<1, 8>(a, tiles, splits, unit, t, part_o, part_ml);
     }
