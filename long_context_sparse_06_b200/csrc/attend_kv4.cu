@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Ar
             *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
         else
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-                make_uint2(pack_bf16x2(o.x * iv, o.y * iv), pack_bf16x2(o.z * iv, o.w * iv));
+                make_uint2(cvt_bf16x2(o.x * iv, o.y * iv), cvt_bf16x2(o.z * iv, o.w * iv));
     }
 }
 
@@ -533,7 +533,7 @@ __device__ __forceinline__ void merge_task(const AttendKv4Args& a, int tiles, in
     for (int r = 0; r < R; ++r) {
         const float4 o = make_float4(acc[r].x * iv, acc[r].y * iv, acc[r].z * iv, acc[r].w * iv);
         if (a.out_dtype == LCS_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + 4 * r) = o;
-        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + 4 * r) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + 4 * r) = make_uint2(cvt_bf16x2(o.x, o.y), cvt_bf16x2(o.z, o.w));
     }
     if (a.lse != nullptr && j0 == 0 && lane < 16)
         a.lse[(int64_t)g * a.H + head] = L > 0.f ? (M + log2f(L)) / kLog2e : -INFINITY;
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         uint8_t* blk = dst + (p >> 1) * kBlk;
                         const int ch = 4 * (p & 1);
                         *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch)) = widen8_cvt(cv.x, s2);
-                        *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 1)) = widen8_perm(cv.y, s2);
+                        *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 1)) = widen8_cvt(cv.y, s2);
                         *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 2)) = widen8_cvt(cv.z, s2);
                         *reinterpret_cast<uint4*>(blk + sw128_off(my_row, ch + 3)) = widen8_perm(cv.w, s2);
                     }
@@ -1008,7 +1008,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     uint32_t pk[8];
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        pk[q] = pack_bf16x2(__uint_as_float(ov[u][2 * q]) * fs, __uint_as_float(ov[u][2 * q + 1]) * fs);
+                        pk[q] = cvt_bf16x2(__uint_as_float(ov[u][2 * q]) * fs, __uint_as_float(ov[u][2 * q + 1]) * fs);
                     reinterpret_cast<uint4*>(rowp + (dim0 + j * 16) * 2)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     reinterpret_cast<uint4*>(rowp + (dim0 + j * 16) * 2)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                 }

@@ -252,7 +252,7 @@ struct LaneBf16 {
         uint32_t t[7];
         constexpr float mid[7] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.f};
 #pragma unroll
-        for (int k = 0; k < 7; ++k) t[k] = pack_bf16x2(mid[k] * sc, mid[k] * sc);
+        for (int k = 0; k < 7; ++k) t[k] = cvt_bf16x2(mid[k] * sc, mid[k] * sc);
         uint32_t w[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -346,7 +346,7 @@ __device__ __forceinline__ void store16(__nv_bfloat16* o, uint2 c, float sc) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float2 a = e2m1x2_to_f32(w >> (8 * k));
-            r[k] = pack_bf16x2(a.x * sc, a.y * sc);
+            r[k] = cvt_bf16x2(a.x * sc, a.y * sc);
         }
         reinterpret_cast<uint4*>(o)[i] = make_uint4(r[0], r[1], r[2], r[3]);
     }
