@@ -476,9 +476,11 @@ __device__ __forceinline__ uint32_t scale_f16x2(uint32_t w, int at) {
 }
 
 // A lane's part of row lane % kRowsPerWarp of its warp's rows of a chunk: the 16-byte pieces p =
-// lane / kRowsPerWarp + kPieces i of the 16 of codes and the 8 of RoPE dims, and the row's scales.
+// lane / kRowsPerWarp + kPieces i of the 16 of codes and the 8 of RoPE dims, and the scales of either
+// half of the columns.
 struct RawRow {
-    uint4 codes[16 / kPieces], rope[8 / kPieces], scales;
+    uint4 codes[16 / kPieces], rope[8 / kPieces];
+    uint2 scales[2];
 };
 
 // Split partials lie as the attention's lanes held them: per unit and split 256 rows of 32 lanes x 16
@@ -619,20 +621,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return e >= 0 && e < lim ? kv4_row(a, b, e) : nullptr;
     };
     RawRow raw;
-    auto load_row = [&](const uint8_t* src) {
+    auto load_half = [&](const uint8_t* src, int hf) {
         const uint4* p = reinterpret_cast<const uint4*>(src) + my_piece;
         if (src != nullptr) {
+            raw.scales[hf] = __ldg(reinterpret_cast<const uint2*>(src + 384) + hf);
 #pragma unroll
-            for (int i = 0; i < 16 / kPieces; ++i) raw.codes[i] = __ldg(p + kPieces * i);
+            for (int i = hf * (8 / kPieces); i < (hf + 1) * (8 / kPieces); ++i) raw.codes[i] = __ldg(p + kPieces * i);
+            if (hf) {
 #pragma unroll
-            for (int i = 0; i < 8 / kPieces; ++i) raw.rope[i] = __ldg(p + 16 + kPieces * i);
-            raw.scales = __ldg(reinterpret_cast<const uint4*>(src) + 24);
+                for (int i = 0; i < 8 / kPieces; ++i) raw.rope[i] = __ldg(p + 16 + kPieces * i);
+            }
         }
     };
     const uint8_t *cur = nullptr, *nxt = nullptr;
     if (producer) {
         cur = row_of(pg, held);
-        load_row(cur);
+        load_half(cur, 0);
+        load_half(cur, 1);
     }
     const Kv4Window wp = kv4_window(a, g, b);
     const int64_t n = kv4_entries(a, b, status);
@@ -821,8 +826,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int i = hf * (8 / kPieces); i < (hf + 1) * (8 / kPieces); ++i) {
                         const int p = my_piece + kPieces * i;
-                        const uint32_t sw = p < 8 ? (p < 4 ? raw.scales.x : raw.scales.y) : (p < 12 ? raw.scales.z : raw.scales.w);
-                        const uint32_t s2 = live ? scale_f16x2(sw, p & 3) : 0u;
+                        const uint32_t sw = i & 1 ? raw.scales[hf].y : raw.scales[hf].x;
+                        const uint32_t s2 = live ? scale_f16x2(sw, my_piece) : 0u;
                         const uint4 cv = live ? raw.codes[i] : make_uint4(0, 0, 0, 0);
                         uint8_t* blk = dst + (p >> 1) * kBlk;
                         const int ch = 4 * (p & 1);
@@ -840,11 +845,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.kfull[st][hf]);
+                    // this half's registers are free: the group's next chunk's rows are asked for at once (asked for after
+                    // both halves, they came 2000 cycles after the group was ready for them)
+                    if (c + kProdGroups < ncc) load_half(nxt, hf);
                 }
                 if (!ok) break;
-                // the group's next chunk's rows into the registers, and where the one after lies
-                cur = nxt;
-                if (c + kProdGroups < ncc) load_row(cur);
+                cur = nxt;   // and where the rows of the one after lie
                 if (c + 2 * kProdGroups < ncc) nxt = row_of(c + 2 * kProdGroups, (int)(sel != nullptr ? n : most));
             }
             if ((st += kProdGroups) >= kStages) st -= kStages, ph ^= 1;
