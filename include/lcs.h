@@ -390,8 +390,14 @@ LCS_API int lcs_kv4_load(const void* pool, int64_t n_slots, const int64_t* slots
  * block and rows behind its last entry may hold anything.  A block id outside [0, n_blocks)
  * records LCS_ERR_DEVICE and leaves that query's output unspecified; n_entries past
  * max_blocks * block_entries records it too and counts as that.
- * d_c, d_r as lcs_kv4_store; d_c = 512, d_r = 64 with bf16 q runs on the tensor cores.  q,
- * pool, win and out on 16 bytes.  Workspace: lcs_workspace_size(LCS_OP_ATTEND_KV4, B, Q, N_c =
+ * d_c, d_r as lcs_kv4_store; d_c = 512, d_r = 64 with bf16 q runs on the tensor cores.  There
+ * the content dims and the weights are fp16 operands: stored rows are exact in it; q is scaled
+ * by a power of two per head (exact down to 2^-28 of the head's largest element); window
+ * content is exact from 2^-14 up, off by at most 2^-25 below, and a magnitude of 2^16 or more
+ * records LCS_ERR_DEVICE; a weight is off by at most 2^-11 of itself.  RoPE dims stay bf16: of
+ * magnitude below 2^100, so that fp32 sums hold (on either path |scale q.K| <= 2^23 and
+ * finite q and attended rows; other outputs are unspecified).  q,
+ * pool, win and out on 16 bytes; max_blocks * block_entries + Tw < 2^31 - 2^16.  Workspace: lcs_workspace_size(LCS_OP_ATTEND_KV4, B, Q, N_c =
  * max_blocks * block_entries, Tw, k (0 for HCA), H, d_v = d_c, 0).
  */
 LCS_API int csa_attend_kv4(const void* q, int q_dtype, const void* pool, int64_t n_blocks, int block_entries,

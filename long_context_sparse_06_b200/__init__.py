@@ -389,13 +389,20 @@ def _dev(t):
 _fns = {}
 
 
-def _call_on(dev, name, stream, *args):
-    """The call on device `dev`: with it current, on `stream` or its current stream."""
+def _on(stream, t):
+    """The context in which a call on tensor `t`, and what it allocates, goes to `stream`."""
+    if stream.device.index != _dev(t):
+        raise ValueError(f"stream: one of {t.device} expected, got one of {stream.device}")
+    return _torch().cuda.stream(stream)
+
+
+def _call_on(dev, name, *args):
+    """The call on device `dev`: with it current, on its current stream."""
     torch = _torch()
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(lib(), name)
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    s = torch._C._cuda_getCurrentRawStream(dev)
     if dev == torch.cuda.current_device():
         rc = fn(*args, s)
     else:
@@ -423,6 +430,9 @@ def lcs_page_plan(lens, n_new, free_blocks, block_table, block_tokens=128, m=4, 
     """lens, n_new [B] int64; free_blocks [n_free] int32; block_table [B, max_blocks] int32, extended in
     place -> (slots [max_slots], offsets [B+1], slots2 [max_slots2], offsets2 [B+1], taken [1]), int64;
     slots2 and offsets2 are None when m2 is 0."""
+    if stream is not None:
+        with _on(stream, lens):
+            return lcs_page_plan(lens, n_new, free_blocks, block_table, block_tokens, m, max_slots, m2, max_slots2, ws)
     torch = _torch()
     i64, i32 = torch.int64, torch.int32
     dev = _dev(lens)
@@ -437,14 +447,14 @@ def lcs_page_plan(lens, n_new, free_blocks, block_table, block_tokens=128, m=4, 
         p = out.data_ptr()
         p2 = p + 8 * max_slots
         po = p2 + 8 * max_slots2
-        _call_on(dev, "lcs_page_plan", stream, *head, m, p, max_slots, po, m2, p2, max_slots2, po + 8 * (B + 1),
+        _call_on(dev, "lcs_page_plan", *head, m, p, max_slots, po, m2, p2, max_slots2, po + 8 * (B + 1),
                  po + 16 * (B + 1), wp, wb)
         return slots, off, slots2, off2, taken
     out = lens.new_empty(max_slots + B + 2)
     slots, off, taken = out.split_with_sizes((max_slots, B + 1, 1))
     p = out.data_ptr()
     po = p + 8 * max_slots
-    _call_on(dev, "lcs_page_plan", stream, *head, m, p, max_slots, po, 0, None, 0, None, po + 8 * (B + 1), wp, wb)
+    _call_on(dev, "lcs_page_plan", *head, m, p, max_slots, po, 0, None, 0, None, po + 8 * (B + 1), wp, wb)
     return slots, off, None, None, taken
 
 
@@ -456,17 +466,23 @@ def _pool_arg(pool, d_c, d_r, dev):
 
 def lcs_kv4_store(x, slots, pool, d_c=512, ws=None, stream=None):
     """Quantises x [n, d_c + d_r] (fp32/bf16) into the pool's 4-bit rows at slots [n] int64 (negative: skipped)."""
+    if stream is not None:
+        with _on(stream, x):
+            return lcs_kv4_store(x, slots, pool, d_c, ws)
     dev = _dev(x)
     n, D = x.shape
     pp, n_slots = _pool_arg(pool, d_c, D - d_c, dev)
     wp, wb, ws = _ws(ws, _status_bytes, dev)
-    _call_on(dev, "lcs_kv4_store", stream, _arg(x, "x", x.dtype, (n, D), dev), _dt(x), n, d_c, D - d_c,
+    _call_on(dev, "lcs_kv4_store", _arg(x, "x", x.dtype, (n, D), dev), _dt(x), n, d_c, D - d_c,
              _arg(slots, "slots", _torch().int64, (n,), dev), pp, n_slots, wp, wb)
     return pool
 
 
 def lcs_kv4_load(pool, slots, d_c=512, d_r=64, out_dtype=None, out=None, ws=None, stream=None):
     """The values of the pool's rows at slots [n] int64 (negative: zeros) -> [n, d_c + d_r] (bf16 or fp32)."""
+    if stream is not None:
+        with _on(stream, pool):
+            return lcs_kv4_load(pool, slots, d_c, d_r, out_dtype, out, ws)
     torch = _torch()
     dev = _dev(pool)
     n = slots.numel()
@@ -474,13 +490,17 @@ def lcs_kv4_load(pool, slots, d_c=512, d_r=64, out_dtype=None, out=None, ws=None
     if out is None:
         out = pool.new_empty((n, d_c + d_r), dtype=out_dtype or torch.bfloat16)
     wp, wb, ws = _ws(ws, _status_bytes, dev)
-    _call_on(dev, "lcs_kv4_load", stream, pp, n_slots, _arg(slots, "slots", torch.int64, (n,), dev), n, d_c, d_r,
+    _call_on(dev, "lcs_kv4_load", pp, n_slots, _arg(slots, "slots", torch.int64, (n,), dev), n, d_c, d_r,
              _arg(out, "out", out_dtype or out.dtype, (n, d_c + d_r), dev), _dt(out), wp, wb)
     return out
 
 
 def _attend_kv4(name, q, pool, block_table, n_entries, win, idx, k, hca_m, scale, d_c, n_win, q_pos, win_pos0, W,
                 want_lse, out_dtype, ws, stream):
+    if stream is not None:
+        with _on(stream, q):
+            return _attend_kv4(name, q, pool, block_table, n_entries, win, idx, k, hca_m, scale, d_c, n_win, q_pos, win_pos0,
+                               W, want_lse, out_dtype, ws, None)
     torch = _torch()
     i64, dt, dev = torch.int64, q.dtype, _dev(q)
     B, Q, H, D = q.shape
@@ -501,9 +521,9 @@ def _attend_kv4(name, q, pool, block_table, n_entries, win, idx, k, hca_m, scale
             *(() if hca_m is None else (hca_m,)), W, H, d_c, D - d_c, scale, out.data_ptr(), BF16 if out.dtype is bf16 else _dt(out),
             None if lse is None else lse.data_ptr(), wp, wb)
     if hca_m is None:
-        _call_on(dev, name, stream, *head, _arg(idx, "idx", torch.int32, (B, Q, k), dev), k, *tail)
+        _call_on(dev, name, *head, _arg(idx, "idx", torch.int32, (B, Q, k), dev), k, *tail)
     else:
-        _call_on(dev, name, stream, *head, *tail)
+        _call_on(dev, name, *head, *tail)
     return (out, lse) if want_lse else out
 
 

@@ -605,6 +605,7 @@ static int run_attend_kv4(const AttendKv4Args& a, void* ws, size_t ws_bytes, cud
     if (a.max_blocks >= (int64_t(1) << 31) / a.be || a.B >= (int64_t(1) << 24) || a.Q >= (int64_t(1) << 31) ||
         a.B * a.Q * 2 >= (int64_t(1) << 31) || a.Tw >= (int64_t(1) << 31) || a.n_blocks >= (int64_t(1) << 31))
         return LCS_ERR_UNSUPPORTED;
+    if (a.max_blocks * a.be + a.Tw >= (int64_t(1) << 31) - (1 << 16)) return LCS_ERR_UNSUPPORTED;   // rows in 32 bits
     if (bad_ws(ws, ws_bytes, kStatusBytes + attend_kv4_scratch_bytes(a))) return LCS_ERR_WORKSPACE;
     if (!device_ok()) return LCS_ERR_CUDA;
     return from_cuda(launch_attend_kv4(a, static_cast<uint8_t*>(ws) + kStatusBytes, status_of(ws), stream));
@@ -766,7 +767,7 @@ int64_t lcs_workspace_size(int op, int64_t B, int64_t Q, int64_t N_c, int64_t Tw
             AttendKv4Args c = a;
             c.k = k;
             c.idx = reinterpret_cast<const int32_t*>(1);
-            const int64_t s1 = attend_kv4_scratch_bytes(a), s2 = attend_kv4_scratch_bytes(c);
+            const int64_t s1 = attend_kv4_scratch_bound(a), s2 = attend_kv4_scratch_bound(c);
             return kStatusBytes + align256(s1 > s2 ? s1 : s2);
         }
         default: return -1;

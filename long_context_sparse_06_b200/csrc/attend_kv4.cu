@@ -30,7 +30,7 @@ __device__ __forceinline__ int64_t kv4_entries(const AttendKv4Args& a, int64_t b
 __device__ __forceinline__ int64_t kv4_avail(const AttendKv4Args& a, int64_t g, int64_t n) {
     if (a.q_pos == nullptr) return n;
     const int64_t p = a.q_pos[g];
-    const int64_t av = p < 0 ? 0 : (p + 1) / a.m;
+    const int64_t av = p < 0 ? 0 : (p < INT64_MAX ? p + 1 : p) / a.m;   // (no sum past 64 bits)
     return av < n ? av : n;
 }
 
@@ -46,8 +46,10 @@ __device__ __forceinline__ Kv4Window kv4_window(const AttendKv4Args& a, int64_t 
         }
         return w;
     }
-    const int64_t t = a.q_pos[g], p0 = a.win_pos0[b];
-    int64_t lo = t - a.W + 1 - p0, hi = t - p0;
+    // the query's own row, counted from the window's first (a difference past 64 bits is of no window row
+    // either way)
+    int64_t hi = (int64_t)((uint64_t)a.q_pos[g] - (uint64_t)a.win_pos0[b]);
+    int64_t lo = hi < 0 ? 0 : hi - a.W + 1;
     if (lo < 0) lo = 0;
     if (hi > a.Tw - 1) hi = a.Tw - 1;
     w.lo = lo;
@@ -799,12 +801,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 if (c != pg) copy_window(c, st);   // the first is on its way
                 cp_async_wait<0>();
+                uint32_t m2 = 0;
 #pragma unroll 4
                 for (int k = 0; k < 64 / kPieces; ++k) {   // a lane's own copies
                     uint4* x = reinterpret_cast<uint4*>(dst + (k >> 1) * kBlk + (k & 1 ? wo1 : wo0));
                     const uint4 v = *x;
+                    m2 = bf16x2_maxabs(m2, bf16x2_maxabs(bf16x2_maxabs(v.x, v.y), bf16x2_maxabs(v.z, v.w)));
                     *x = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
                 }
+                // a magnitude of 2^16 or more does not fit
+                if (max(m2 & 0x7FFFu, (m2 >> 16) & 0x7FFFu) >= 0x4780u) set_status(status, LCS_ERR_DEVICE, 614);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -1079,11 +1085,11 @@ bool use_tc(const AttendKv4Args& a) { return a.q_dtype == LCS_BF16 && a.d_c == k
 // splits: 4 chunks of one query 14.1 (1), 16.1 (2); 14 chunks of 32 queries 25.9 (2), 23.4 (3), 20.4
 // (4); 25 of 4: 20.6 (8), 17.7 (9), 16.4 (13); 177 of one 26.7 (16), 22.1 (29), 20.8 (58); 177 of
 // 16: 40.2 (8, clusters), 39.4 (9, merged by a kernel).
-int kv4_splits(const AttendKv4Args& a) {
-    const int64_t units = a.B * a.Q * ((a.H + kH - 1) / kH);
-    const int64_t most_w = a.q_pos == nullptr ? a.Tw : (a.W < a.Tw ? a.W : a.Tw);
-    const int64_t chunks = (most_w + kChunk - 1) / kChunk +
-                           ((a.idx != nullptr ? a.k : a.max_blocks * a.be) + kChunk - 1) / kChunk;
+int64_t kv4_units(const AttendKv4Args& a) { return a.B * a.Q * ((a.H + kH - 1) / kH); }
+int64_t kv4_entry_chunks(const AttendKv4Args& a) {
+    return ((a.idx != nullptr ? a.k : a.max_blocks * a.be) + kChunk - 1) / kChunk;
+}
+int kv4_splits_of(int64_t units, int64_t chunks) {
     int best = 1;
     double best_cost = (double)chunks;
     for (int s = 2; s <= kMaxSplits && s <= chunks && units * s <= num_sms(); ++s) {
@@ -1095,6 +1101,14 @@ int kv4_splits(const AttendKv4Args& a) {
         }
     }
     return best;
+}
+int kv4_splits(const AttendKv4Args& a) {
+    const int64_t most_w = a.q_pos == nullptr ? a.Tw : (a.W < a.Tw ? a.W : a.Tw);
+    return kv4_splits_of(kv4_units(a), (most_w + kChunk - 1) / kChunk + kv4_entry_chunks(a));
+}
+// Split partials: fp32 O [units, splits, 64, 512] and (m, l) [units, splits, 64, 2].
+int64_t kv4_partial_bytes(int64_t units, int64_t splits) {
+    return splits == 1 ? 0 : align256(units * splits * kH * kDv * 4) + align256(units * splits * kH * 2 * 4);
 }
 
 // Whether the launch's clusters of `splits` CTAs can all be resident at once (asked once per device and
@@ -1132,7 +1146,7 @@ bool kv4_cluster_ok(int splits, int64_t units) {
 
 cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaStream_t s) {
     const int tiles = (a.H + kH - 1) / kH;
-    const int64_t units = a.B * a.Q * tiles;
+    const int64_t units = kv4_units(a);
     cudaError_t e = set_smem_here(reinterpret_cast<const void*>(attend_kv4_tc_kernel), kTcSmem);
     if (e != cudaSuccess) return e;
     const int splits = kv4_splits(a);
@@ -1166,13 +1180,27 @@ cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaSt
 
 }  // namespace
 
-// Split partials: fp32 O [units, splits, 64, 512] and (m, l) [units, splits, 64, 2].
 int64_t attend_kv4_scratch_bytes(const AttendKv4Args& a) {
-    if (!use_tc(a)) return 0;
-    const int s = kv4_splits(a);
-    if (s == 1) return 0;
-    const int64_t units = a.B * a.Q * ((a.H + kH - 1) / kH);
-    return align256(units * s * kH * kDv * 4) + align256(units * s * kH * 2 * 4);
+    return use_tc(a) ? kv4_partial_bytes(kv4_units(a), kv4_splits(a)) : 0;
+}
+
+// The most that a call of these sizes needs, whatever its W: fewer window rows can mean more splits (the
+// longest split's chunks are rounded up).  Short windows: every chunk count.  Long ones: as many splits
+// as there can be.
+int64_t attend_kv4_scratch_bound(const AttendKv4Args& a) {
+    if (!use_tc(a) || a.B * a.Q <= 0) return 0;
+    const int64_t units = kv4_units(a), entries = kv4_entry_chunks(a), window = (a.Tw + kChunk - 1) / kChunk;
+    int64_t s = 1;
+    if (window <= 8) {
+        for (int64_t w = window > 0; w <= window; ++w) {
+            const int64_t x = kv4_splits_of(units, entries + w);
+            s = x > s ? x : s;
+        }
+    } else if (units * 2 <= num_sms()) {
+        s = num_sms() / units < kMaxSplits ? num_sms() / units : kMaxSplits;
+        if (s > entries + window) s = entries + window;
+    }
+    return kv4_partial_bytes(units, s);
 }
 
 cudaError_t launch_attend_kv4(const AttendKv4Args& a, void* scratch, int* status, cudaStream_t s) {

@@ -108,6 +108,7 @@ struct AttendKv4Args {
     float* lse;
 };
 int64_t attend_kv4_scratch_bytes(const AttendKv4Args& a);
+int64_t attend_kv4_scratch_bound(const AttendKv4Args& a);   // over every W
 cudaError_t launch_attend_kv4(const AttendKv4Args& a, void* scratch, int* status, cudaStream_t s);
 
 // cp.cu -- context parallelism for one long request (entries split over ranks)

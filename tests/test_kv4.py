@@ -10,8 +10,8 @@ Tolerances (derived, per element, from the data of the test):
     path sums D terms with a rounding of 2^-24 each: D * 2^-24 in place of (D/16 + 2) * 2^-23);
   * a weight p_r / l then has the relative error 2 delta (its own and the sum's) + 2^-21 (exp2 and
     the scaling of its argument: arguments up to 2^5 lose 2^-24 * 2^5 = 2^-19: counted as 2^-18),
-    plus its own rounding: 2^-11 (fp16) for compressed rows, 2^-8 (bf16) for window rows, none on the
-    CUDA cores; weights below the smallest fp16 step 2^-24 / 2^6 of the largest lose that much
+    plus its own rounding, 2^-11 (fp16; none on the CUDA cores); window content below 2^-14 is
+    off by 2^-25 on the tensor cores (fp16's subnormals); weights below the smallest fp16 step 2^-24 / 2^6 of the largest lose that much
     absolutely; the sum over R rows in fp32 adds (R/16 + 2) * 2^-23 of sum p|v|;
   * a bf16 output is off by half a step, 2^-8 |o|; fp32 by 2^-24 |o|.
 """
@@ -87,17 +87,19 @@ def attend_ref(q, K, n_comp, d_c, scale, tc):
     s = (q @ K.T) * scale
     mags = (q.abs() @ K.abs().T) * abs(scale)
     delta = mags * ((D / 16 + 2) * 2.0 ** -23 if tc else D * 2.0 ** -24) + s.abs() * 2.0 ** -22
+    if tc:
+        delta[:, n_comp:] += abs(scale) * q.abs().sum(-1, keepdim=True) * 2.0 ** -25
     p = torch.softmax(s, -1)
     V = K[:, :d_c]
     o = p @ V
+    off = p[:, n_comp:].sum(-1, keepdim=True) * 2.0 ** -25 if tc else 0.0
     dmax = delta.amax(-1, keepdim=True)
     rel = 2 * dmax + 2.0 ** -18 + torch.zeros_like(s)
     if tc:
-        rel[:, :n_comp] += 2.0 ** -11
-        rel[:, n_comp:] += 2.0 ** -8
+        rel += 2.0 ** -11
     rel = rel + (R / 16 + 2 if tc else R) * 2.0 ** -23
     pa = p * rel + ((2.0 ** -31) * p.amax(-1, keepdim=True) if tc else 0.0)
-    bound = pa @ V.abs() + 1e-30
+    bound = pa @ V.abs() + off + 1e-30
     return o, bound, torch.logsumexp(s, -1), dmax[:, 0] + 2.0 ** -18 + torch.logsumexp(s, -1).abs() * 2.0 ** -22
 
 
@@ -159,7 +161,8 @@ def test_refusals_without_device(L):
                     dict(qp=P), dict(wp=P), dict(qp=P, wp=P, nw=P), dict(q=P + 2), dict(pool=P + 8), dict(win=P + 8),
                     dict(out=P + 4), dict(Tw=-1), dict(mb=-1), dict(nb=-1)):
             assert f(**bad) == -1, (f.__name__, bad)
-        for bad in (dict(H=129), dict(qd=2), dict(qd=4), dict(od=2), dict(mb=1 << 27), dict(B=1 << 24), dict(nb=1 << 31)):
+        for bad in (dict(H=129), dict(qd=2), dict(qd=4), dict(od=2), dict(mb=1 << 27), dict(B=1 << 24), dict(nb=1 << 31),
+                    dict(be=1, mb=(1 << 31) - (1 << 16) - 128), dict(Tw=(1 << 31) - (1 << 16))):
             assert f(**bad) == -2, (f.__name__, bad)
         for bad in (dict(ws=None), dict(wb=16), dict(ws=P + 64)):
             assert f(**bad) == -6, (f.__name__, bad)
@@ -171,6 +174,21 @@ def test_refusals_without_device(L):
         assert plan() == -3 and csa() == -3 and hca() == -3
         assert lib.lcs_kv4_store(P, 0, 4, 512, 64, P, P, 8, P, 256, None) == -3
         assert lib.lcs_kv4_load(P, 8, P, 4, 512, 64, P, 1, P, 256, None) == -3
+
+
+def test_the_workspace_size_covers_every_window(L):
+    """Fewer window rows can mean more splits: lcs_workspace_size holds for any W up to Tw."""
+    if torch.cuda.is_available():
+        pytest.skip("fake addresses: only where nothing can be launched")
+    lib, P = L.lib(), 4096
+    for B, Q, N, Tw, k, H in ((1, 1, 200, 384, 64, 64), (1, 1, 1500, 300, 500, 128), (4, 1, 900, 128, 300, 64), (3, 1, 4000, 5000, 100, 64),
+                              (2, 3, 700, 240, 333, 64), (9, 1, 640, 200, 512, 64), (1, 1, 0, 600, 0, 64)):
+        size = L.lcs_workspace_size(L.OP_ATTEND_KV4, B, Q, N, Tw, k, H, 512)
+        for W in range(1, Tw + 30, 7):
+            args = (P, 1, P, 9, 1, P, N, P, P, None, B, Q, Tw)
+            dims = (H, 512, 64, 0.1, P, 1, None, P, size, None)
+            assert lib.csa_attend_kv4(*args, P, k, P, P, W, *dims) == -3, (B, Q, N, Tw, W)
+            assert lib.hca_attend_kv4(*args, P, P, 4, W, *dims) == -3, (B, Q, N, Tw, W)
 
 
 def test_binding_refuses_cpu_and_mismatched_tensors(L):
@@ -389,7 +407,7 @@ def case(L, op, B, N, be, H, d_c, d_r, dt, Tw=128, k=0, ragged=None, n_win=None,
     qp = torch.tensor(q_pos, device=DEV) if q_pos is not None else None
     wp = torch.tensor(win_pos0, device=DEV) if win_pos0 is not None else None
     nw = torch.tensor(n_win, device=DEV) if n_win is not None else None
-    seen = lens[:, None].expand(B, Q) if qp is None else torch.minimum(lens[:, None].expand(B, Q), ((qp + 1) // m).clamp(min=0))
+    seen = lens[:, None].expand(B, Q) if qp is None else torch.minimum(lens[:, None].expand(B, Q), (qp // m + (qp % m == m - 1)).clamp(min=0))
     idx = None
     if op == "csa":
         idx = torch.full((B, Q, k), -1, dtype=torch.int32, device=DEV)
@@ -751,6 +769,173 @@ def test_other_stream_and_graph(G):
             assert torch.equal(u, v)
         assert torch.equal(tab, t2)
     assert G.lcs_status(ws2) == 0 and G.lcs_status(ws3) == 0
+
+
+@gpu
+@pytest.mark.parametrize("d_c,d_r,dt", [(512, 64, BF), (64, 16, torch.float32)])
+def test_positions_of_any_size(G, d_c, d_r, dt):
+    """Positions up to the type's ends: every entry, no window row; before everything: nothing."""
+    top, low = (1 << 63) - 1, -(1 << 63)
+    case(G, "hca", 1, 50, 4, 8, d_c, d_r, dt, Tw=30, Q=5, q_pos=[[top, top - 1, 1 << 62, low, -5]], win_pos0=[0], m=3, seed=1)
+    case(G, "csa", 1, 50, 4, 8, d_c, d_r, dt, Tw=30, k=20, Q=3, q_pos=[[top, 1 << 62, -5]], win_pos0=[0], m=3, seed=2)
+
+
+@gpu
+def test_window_values_past_fp16(G):
+    """Window content of up to 65280 (bf16's last below 2^16) is exact in fp16; from 2^16 on it is an error."""
+    pool = make_pool(G, 4, 16, 512, 64, 3)
+    table, n = torch.arange(4, dtype=torch.int32, device=DEV).view(1, 4), torch.tensor([20], device=DEV)
+    q = torch.randn((1, 1, 64, 576), generator=gen(1), device=DEV).to(BF)
+    win = torch.randn((1, 60, 576), generator=gen(2), device=DEV).to(BF)
+    win[0, 50, 7], win[0, 3, 511], win[0, 9, 530] = 65280.0, -65280.0, 2.0 ** 20    # (RoPE dims stay bf16)
+    ws = G.workspace(G.lcs_workspace_size(G.OP_ATTEND_KV4, 1, 1, 64, 60, 0))
+    o, lse = G.hca_attend_kv4(q, pool, table, n, win, 1e-5, want_lse=True, ws=ws)
+    assert G.lcs_status(ws) == 0
+    K = torch.cat((decode_rows(pool.view(64, -1)[:20], 512, 64), win[0].double()))
+    check(o[0, 0], lse[0, 0], attend_ref(q[0, 0], K, 20, 512, 1e-5, True), True, "large window values")
+    for v in (65536.0, -3e38, math.inf):
+        w = win.clone()
+        w[0, 59, 0] = v
+        G.hca_attend_kv4(q, pool, table, n, w, 1e-5, ws=ws)
+        assert G.lcs_status(ws) == -5
+        G.hca_attend_kv4(q, pool, table, n, w, 1e-5, n_win=torch.tensor([59], device=DEV), ws=ws)   # not attended
+        assert G.lcs_status(ws) == 0
+
+
+@gpu
+def test_selections_made_just_before(G):
+    """Top-k and the attention over its selection, step after step on the same buffers without a pause."""
+    B, N, k = 8, 3000, 128
+    pool = make_pool(G, B * 94, 32, 512, 64, 6)
+    table = torch.randperm(B * 94, generator=gen(1), device=DEV, dtype=torch.int32).view(B, 94).contiguous()
+    n = torch.full((B,), N, device=DEV)
+    q = torch.randn((B, 1, 64, 576), generator=gen(2), device=DEV).to(BF)
+    win = torch.randn((B, 128, 576), generator=gen(3), device=DEV).to(BF)
+    steps = [torch.randn((B, 1, N), generator=gen(10 + i), device=DEV) for i in range(12)]
+    ws = G.workspace(G.lcs_workspace_size(G.OP_ATTEND_KV4, B, 1, 94 * 32, 128, k))
+    idx = torch.full((B, 1, k), -1, dtype=torch.int32, device=DEV)
+    tws = G.workspace(max(256, G.lcs_workspace_size(G.OP_TOPK, B, 1, N, k=k)))
+    pos = torch.full((B, 1), 4 * N - 1, device=DEV)
+
+    def step(s):
+        G._call("lcs_topk", s.data_ptr(), G.F32, B, 1, N, pos.data_ptr(), 4, k, idx.data_ptr(), tws.data_ptr(), tws.numel(),
+                torch.cuda.current_stream().cuda_stream)
+        return G.csa_attend_kv4(q, pool, table, n, win, idx, 1 / 24, ws=ws)
+
+    want = []
+    for s in steps:
+        want.append(step(s))
+        torch.cuda.synchronize()
+    got = [step(s) for s in steps]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = [step(s) for s in steps]
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b, c in zip(want, got, held):
+        assert torch.equal(a, b) and torch.equal(a, c)
+    assert G.lcs_status(ws) == 0
+
+
+@gpu
+def test_one_workspace_for_calls_in_turn(G):
+    """Calls of different sizes and split counts, one after the other on one workspace."""
+    pool = make_pool(G, 300, 32, 512, 64, 7)
+    mk = lambda B, seed: (torch.randn((B, 1, 64, 576), generator=gen(seed), device=DEV).to(BF),
+                          torch.randint(0, 300, (B, 280), generator=gen(seed), device=DEV, dtype=torch.int32),
+                          torch.randint(0, 280 * 32, (B,), generator=gen(seed), device=DEV),
+                          torch.randn((B, 128, 576), generator=gen(seed), device=DEV).to(BF))
+    sets = [mk(B, B) for B in (1, 16, 3, 150, 2, 40)]
+    ws = G.workspace(max(G.lcs_workspace_size(G.OP_ATTEND_KV4, B, 1, 280 * 32, 128, 0) for B in (1, 16, 3, 150, 2, 40)))
+    alone = [G.hca_attend_kv4(q, pool, t, n, w, 1 / 24, out_dtype=torch.float32) for q, t, n, w in sets]
+    torch.cuda.synchronize()
+    turn = [G.hca_attend_kv4(q, pool, t, n, w, 1 / 24, out_dtype=torch.float32, ws=ws) for q, t, n, w in sets * 3]
+    for i, o in enumerate(turn):
+        assert torch.equal(o, alone[i % len(sets)])
+    assert G.lcs_status(ws) == 0
+
+
+@gpu
+def test_stream_argument_without_a_workspace(G):
+    """What the call allocates belongs to the given stream: work on the current one does not touch it."""
+    pool = make_pool(G, 64, 32, 512, 64, 8)
+    table, n = torch.arange(64, dtype=torch.int32, device=DEV).view(1, 64), torch.tensor([2000], device=DEV)
+    q = torch.randn((1, 1, 64, 576), generator=gen(2), device=DEV).to(BF)
+    x, slots = torch.randn((40, 576), generator=gen(3), device=DEV), torch.arange(40, device=DEV)
+    want, rows = G.hca_attend_kv4(q, pool, table, n, None, 1 / 24), G.lcs_kv4_load(pool, slots)
+    big = torch.randn((4096, 4096), device=DEV)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        big @ big                                   # the current stream is busy when the calls are made
+        a, b = G.hca_attend_kv4(q, pool, table, n, None, 1 / 24, stream=st), G.lcs_kv4_load(pool, slots, stream=st)
+        st.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, rows)
+    own = torch.zeros((64, 400), dtype=torch.uint8, device=DEV)
+    tab = torch.full((1, 4), -1, dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    G.lcs_kv4_store(x, slots, own, stream=st)
+    plan = G.lcs_page_plan(torch.tensor([0], device=DEV), torch.tensor([300], device=DEV), torch.tensor([5, 2, 9], dtype=torch.int32, device=DEV),
+                           tab, max_slots=75, stream=None)
+    st.synchronize()
+    assert torch.equal(G.lcs_kv4_load(own, slots, out_dtype=torch.float32).double(), decode_rows(own[:40], 512, 64))
+    assert tab.tolist() == [[5, 2, 9, -1]] and plan[4].item() == 3
+
+
+@gpu
+def test_views_that_do_not_fit_are_refused(G):
+    pool = make_pool(G, 4, 16, 512, 64, 3)
+    table, n = torch.arange(4, dtype=torch.int32, device=DEV).view(1, 4), torch.tensor([20], device=DEV)
+    q = torch.randn((1, 1, 64, 576), device=DEV).to(BF)
+    with pytest.raises(ValueError):
+        G.hca_attend_kv4(q.transpose(2, 3).contiguous().transpose(2, 3), pool, table, n, None, 0.1)
+    with pytest.raises(ValueError):
+        G.hca_attend_kv4(q, pool[:, ::2], table, n, None, 0.1)
+    with pytest.raises(ValueError):
+        G.hca_attend_kv4(q, pool, table.view(4, 1).expand(4, 2)[:1], n.float(), None, 0.1)
+    with pytest.raises(ValueError):
+        G.lcs_kv4_store(torch.randn((4, 600), device=DEV)[:, :576], torch.arange(4, device=DEV), pool)
+    off = torch.empty(64 * 576 + 4, dtype=BF, device=DEV)[4:].view(1, 1, 64, 576)     # 8 bytes off
+    with pytest.raises(G.LcsError):
+        G.hca_attend_kv4(off, pool, table, n, None, 0.1)
+    with pytest.raises(G.LcsError):
+        G.hca_attend_kv4(q, pool, table, n, None, 0.1, ws=G.workspace(512)[8:264])
+    with pytest.raises(G.LcsError):
+        G.hca_attend_kv4(q.half().to(BF), pool, table, n, None, 0.1, q_pos=torch.tensor([[4]], device=DEV))   # win_pos0 missing
+
+
+@gpu
+def test_first_call_inside_a_capture(G):
+    """A process whose first calls are captured ones."""
+    import subprocess
+    import sys
+    code = """
+import torch, long_context_sparse_06_b200 as L
+L.lib()
+g = torch.Generator('cuda').manual_seed(1)
+pool = torch.zeros((64, 32, 400), dtype=torch.uint8, device='cuda')
+x = torch.randn((2048, 576), generator=g, device='cuda')
+slots = torch.arange(2048, device='cuda')
+table = torch.arange(64, dtype=torch.int32, device='cuda').view(1, 64)
+n = torch.tensor([2000], device='cuda')
+q = torch.randn((1, 1, 64, 576), generator=g, device='cuda').bfloat16()
+ws = L.workspace(L.lcs_workspace_size(L.OP_ATTEND_KV4, 1, 1, 2048, 0, 0))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    L.lcs_kv4_store(x, slots, pool, ws=ws)
+    o = L.hca_attend_kv4(q, pool, table, n, None, 1 / 24, ws=ws)
+    p = L.hca_attend_kv4(q.float(), pool, table, n, None, 1 / 24, ws=ws)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(o, L.hca_attend_kv4(q, pool, table, n, None, 1 / 24))
+assert (o.float() - p).abs().max() < 0.05 and p.abs().max() > 0.01
+assert L.lcs_status(ws) == 0
+print('captured')
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
+    assert "captured" in r.stdout, r.stdout + r.stderr
 
 
 @gpu
