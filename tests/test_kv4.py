@@ -222,7 +222,7 @@ def run_plan(L, lens, new, free, table, P, m, ms, m2=0, ms2=0, ws=None):
 @gpu
 @pytest.mark.parametrize("B,P,m,m2,most", [(1, 128, 4, 128, 1), (1, 128, 4, 128, 1000), (3, 128, 4, 128, 300), (33, 128, 4, 0, 700),
                                            (7, 4, 4, 2, 9), (5, 1, 1, 0, 6), (511, 128, 4, 128, 200), (512, 16, 4, 8, 40),
-                                           (513, 128, 128, 4, 260), (8192, 128, 4, 128, 12)])
+                                           (513, 128, 128, 4, 260), (8192, 128, 4, 128, 12), (4094, 128, 4, 128, 9), (4095, 128, 4, 128, 9)])
 def test_page_plan(G, B, P, m, m2, most):
     rng = np.random.RandomState(B + most)
     lens = rng.randint(0, 3 * P + 5, B).tolist()
@@ -444,7 +444,8 @@ def case(L, op, B, N, be, H, d_c, d_r, dt, Tw=128, k=0, ragged=None, n_win=None,
 
 
 SMALL = [(8, 64, 16, torch.float32), (1, 32, 0, torch.float32), (3, 96, 32, torch.bfloat16), (13, 32, 8, torch.bfloat16),
-         (128, 64, 16, torch.float32), (9, 512, 64, torch.float32), (5, 480, 128, torch.bfloat16)]
+         (128, 64, 16, torch.float32), (9, 512, 64, torch.float32), (5, 480, 128, torch.bfloat16), (16, 128, 32, torch.float32),
+         (8, 256, 64, torch.bfloat16), (17, 160, 0, torch.float32)]
 
 
 @gpu
@@ -454,6 +455,15 @@ def test_small_shapes(G, op, H, d_c, d_r, dt):
     """The CUDA-core shapes: ragged requests (one empty, one with a window alone), odd pages."""
     case(G, op, 4, 70, 7, H, d_c, d_r, dt, Tw=19, k=33, ragged=[70, 0, 31, 1], n_win=[19, 5, 0, 1], seed=H)
     case(G, op, 2, 40, 1, H, d_c, d_r, dt, Tw=0, k=40, ragged=[0, 40], seed=H + 1, out_dtype=torch.float32)
+
+
+@gpu
+@pytest.mark.parametrize("H,d_c,d_r,dt", SMALL)
+def test_small_shapes_over_many_rows(G, H, d_c, d_r, dt):
+    """Few queries and long row lists: their rows are split; many queries: they are not."""
+    case(G, "hca", 1, 1500, 16, H, d_c, d_r, dt, Tw=100, seed=H)
+    case(G, "csa", 3, 900, 16, H, d_c, d_r, dt, Tw=40, k=300, ragged=[900, 17, 280], n_win=[40, 0, 3], seed=H + 1)
+    case(G, "hca", 170, 20, 4, H, d_c, d_r, dt, Tw=9, ragged=[b % 21 for b in range(170)], n_win=[b % 10 for b in range(170)], seed=H + 2)
 
 
 @gpu
