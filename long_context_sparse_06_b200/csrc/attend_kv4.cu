@@ -67,181 +67,344 @@ __device__ __forceinline__ const uint8_t* kv4_row(const AttendKv4Args& a, int64_
 }
 
 // ------------------------------------------------------------ CUDA-core path
-// Every shape: H <= 128, d_c % 32 == 0 and <= 512, d_r <= 128, fp32 or bf16 queries.  One CTA per
-// query and group of 8 heads: 64 rows at a time widened to fp32 in shared memory; a warp per head
-// forms the scores of two rows a lane (16-byte reads: a row's pitch of D + 4 floats puts a quarter
-// warp's eight rows on different banks) and runs the online softmax; for the outputs a thread
-// holds 4 dims of a head, and threads left over share the rows (summed at the end).  Bound by
-// latency: the rows' addresses are fetched one step ahead.  It serves the small shapes: 1024 causal
-// queries of 8 heads, D = 80, up to 192 rows each.
-constexpr int kSThreads = 256, kSRows = 64, kSHeads = 8;
-constexpr int kSMaxDc = 512;
+// Every shape: H <= 128, d_c % 32 == 0 and <= 512, d_r <= 128, fp32 or bf16 queries.  A CTA serves one
+// query and group of 8 heads (and one of the splits of its rows, which form a cluster); its warps work
+// alone, each on 16 rows at a time with an online softmax of its own, and join their partials at the
+// end.  Shared-memory reads are what it runs out of, so both products reuse what they read:
+//   S: a lane holds rows r, r + 8 and two heads; a warp's read of 4 dims is 8 rows and 8 heads, each
+//      once (a pitch of D + 4 floats puts the eight on different banks) for 512 multiply-adds;
+//   O: a lane holds 4 dims of 8 / G heads, kPass times 128 / G dims apart; a row's dims are read once for
+//      all of them, its weights in one or two 16-byte broadcasts.
+// (A CTA that stepped through 64 rows together, a warp per head, read each row eight times.)  Measured,
+// before and now: 1024 causal fp32 queries of 8 heads, 64 + 16 dims, 192 rows each 58.6 and 32.1 us
+// (without S 22, without O 26, without the window's copies 29); one fp32 query of 64 heads, 512 + 64
+// dims, over 8320 rows 3251 and 184 us (clusters of 8); 128 such queries of 328 rows 1271 and 546 us.
+// Registers: 64 a thread for up to 128 dims (80: 34.4 us); packed fp32 pairs halve the multiply-adds.
+constexpr int kSRows = 16, kSHeads = 8;
+constexpr int kSMaxCluster = 8;
 
-__device__ __forceinline__ float ld_elem(const void* p, int64_t i, int dtype) {
-    return dtype == LCS_F32 ? static_cast<const float*>(p)[i]
-                            : bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
+// Two floats and the packed operations on them: one instruction for both.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
-    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float4 axpy4(float p, float4 v, float4 o) {
+    return make_float4(fmaf(p, v.x, o.x), fmaf(p, v.y, o.y), fmaf(p, v.z, o.z), fmaf(p, v.w, o.w));
+}
+__device__ __forceinline__ float4 scale4(float4 v, float f) { return make_float4(v.x * f, v.y * f, v.z * f, v.w * f); }
+// Eight bf16 -> eight floats.
+__device__ __forceinline__ void put_bf16x8(float* o, uint4 w) {
+    reinterpret_cast<float4*>(o)[0] = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                                                  __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+    reinterpret_cast<float4*>(o)[1] = make_float4(__uint_as_float(w.z << 16), __uint_as_float(w.z & 0xFFFF0000u),
+                                                  __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xFFFF0000u));
 }
 
-// kItems: output pieces (4 dims of a head) per thread, at least 8 d_c / 4 / 256.
-template <int kItems>
-__global__ void __launch_bounds__(kSThreads) attend_kv4_kernel(const AttendKv4Args a, int* status) {
+// Floats of shared memory: q, then per warp its rows, weights and (m, l) of the heads.
+__host__ __device__ constexpr int simt_warp_floats(int D) { return kSRows * (D + 4) + kSRows * kSHeads + 2 * kSHeads; }
+
+template <int G, int kPass>
+__global__ void __launch_bounds__(256, kPass == 1 ? 4 : 1) attend_kv4_kernel(const AttendKv4Args a, int splits, int* status) {
     extern __shared__ float4 sh4[];
     float* sh = reinterpret_cast<float*>(sh4);
-    const int D = a.d_c + a.d_r, pitch = D + 4;
-    float* qs = sh;                            // [heads, D]
-    float* rows = qs + kSHeads * D;            // [64, D + 4]
-    float* sc = rows + kSRows * pitch;         // [heads, 64] weights of this chunk
-    __shared__ float al[kSHeads], lh[kSHeads];
-    __shared__ const uint8_t* ptr[2][kSRows];
+    const int D = a.d_c + a.d_r, pitch = D + 4, c4n = a.d_c / 4;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = blockDim.x >> 5;
+    const int wf = simt_warp_floats(D);
+    float* qs = sh;                              // [8, D + 4]
+    float* rows = qs + kSHeads * pitch + warp * wf;   // [16, D + 4]
+    float* wt = rows + kSRows * pitch;           // [16, 8] weights
+    float* ml = wt + kSRows * kSHeads;           // [2, 8]: rescaling factors; at the end m and l
     __shared__ int nsel_s;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    __shared__ float joint[2][kSHeads];          // this CTA's m and l
     const int64_t g = blockIdx.x, b = g / a.Q;
-    const int h0 = blockIdx.y * kSHeads, nh = min(kSHeads, a.H - h0);
+    const int h0 = blockIdx.y * kSHeads, nh = min(kSHeads, a.H - h0), sp = blockIdx.z;
 
-    for (int i = t; i < kSHeads * D; i += kSThreads)
-        qs[i] = i < nh * D ? ld_elem(a.q, (g * a.H + h0) * D + i, a.q_dtype) : 0.f;
+    for (int i = t; i < kSHeads * (D / 8); i += blockDim.x) {
+        const int h = i / (D / 8), c = i - h * (D / 8);
+        float* o = qs + h * pitch + 8 * c;
+        const int64_t at = (g * a.H + h0 + h) * D + 8 * c;
+        if (h >= nh) {
+            reinterpret_cast<float4*>(o)[0] = reinterpret_cast<float4*>(o)[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else if (a.q_dtype == LCS_F32) {
+            const float4* q4 = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+            reinterpret_cast<float4*>(o)[0] = __ldg(q4);
+            reinterpret_cast<float4*>(o)[1] = __ldg(q4 + 1);
+        } else {
+            put_bf16x8(o, __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at)));
+        }
+    }
     const int64_t n = kv4_entries(a, b, status);
     const int32_t* sel = a.idx != nullptr ? a.idx + g * a.k : nullptr;
     if (t == 0) nsel_s = sel != nullptr ? a.k : (int)kv4_avail(a, g, n);
     __syncthreads();
-    if (sel != nullptr)
-        for (int i = t; i < a.k; i += kSThreads) {
-            const int32_t v = sel[i];
-            if (v < 0 || v >= n) atomicMin(&nsel_s, i);
+    if (sel != nullptr) {
+        int bad = a.k;
+        for (int i = t; i < a.k && bad == a.k; i += blockDim.x) {
+            const int32_t v = __ldg(sel + i);
+            if (v < 0 || v >= n) bad = i;
         }
+        bad = __reduce_min_sync(0xffffffffu, bad);
+        if (lane == 0 && bad < a.k) atomicMin(&nsel_s, bad);
+    }
     __syncthreads();
     const int nsel = nsel_s;
     if (sel != nullptr && t == 0 && nsel < a.k && sel[nsel] >= 0) set_status(status, LCS_ERR_DEVICE, 603);
     const Kv4Window win = kv4_window(a, g, b);
     const int R = nsel + (int)win.n;
-    // address of list row r: a compressed row (null if its block is not one of the pool's) or a window row
+    const int my = lane & 15, half = lane >> 4;   // this lane's row of a block, and every other piece of it
+    // window rows lie one after the other: pieces of 16 bytes of them, lane + 32 i: row and column
+    const int esz = a.q_dtype == LCS_F32 ? 4 : 2, pieces = D * esz / 16;
+    const int wr0 = lane / pieces, wc0 = lane - wr0 * pieces, wrs = 32 / pieces, wcs = 32 - wrs * pieces;
+    const uint8_t* wrows = static_cast<const uint8_t*>(a.win) + (b * a.Tw + win.lo) * D * esz;
+    // address of list row r, a compressed one (null if there is none, or its block is not one of the pool's)
     auto row_at = [&](int r) -> const uint8_t* {
-        if (r >= R) return nullptr;
-        if (r >= nsel)
-            return static_cast<const uint8_t*>(a.win) + (b * a.Tw + win.lo + (r - nsel)) * D * (a.q_dtype == LCS_F32 ? 4 : 2);
+        if (r >= nsel) return nullptr;
         const uint8_t* p = kv4_row(a, b, sel != nullptr ? __ldg(sel + r) : r);
         if (p == nullptr) set_status(status, LCS_ERR_DEVICE, 602);
         return p;
     };
-    if (t < kSRows) ptr[0][t] = row_at(t);
+    const int stride = nw * splits * kSRows;
+    int r0 = (sp * nw + warp) * kSRows;
+    const uint8_t* nxt = row_at(r0 + my);
 
-    // outputs: item j = (head, 4 dims) of nh d_c / 4; `share` threads split an item's rows
-    const int c4n = a.d_c / 4, items = nh * c4n;
-    int share = 1;
-    while (share < 32 && items * share * 2 <= kSThreads) share *= 2;
-    const int part = t % share, first = t / share, step = kSThreads / share;
-    float4 acc[kItems];
+    constexpr int kH8 = kSHeads / G, kSpan = 32 / G;
+    const int grp = lane / kSpan, col = lane % kSpan;
+    uint64_t acc[kPass][kH8][2];
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m = -INFINITY, l = 0.f;              // of head `warp`, the same in every lane
-    __syncthreads();
-    for (int r0 = 0, k = 0; r0 < R; r0 += kSRows, k ^= 1) {
-        const int nr = min(kSRows, R - r0), nc = max(0, min(nr, nsel - r0));   // rows, compressed ones among them
-        if (t < kSRows) ptr[k ^ 1][t] = row_at(r0 + kSRows + t);
-        const int c16 = a.d_c / 16;
-        for (int i = t; i < nc * c16; i += kSThreads) {
-            const int r = i / c16, c = i - r * c16;
-            const uint8_t* src = ptr[k][r];
-            float4* o = reinterpret_cast<float4*>(rows + r * pitch + 16 * c);
-            const uint2 w = src != nullptr ? __ldg(reinterpret_cast<const uint2*>(src) + c) : make_uint2(0, 0);
-            const float s = src != nullptr ? e4m3_to_f32(__ldg(src + a.d_c / 2 + 2 * a.d_r + c / 2)) : 0.f;
+    for (int i = 0; i < kPass; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t x = (q < 2 ? w.x : w.y) >> (16 * (q & 1));
-                const float2 u = e2m1x2_to_f32(x), v = e2m1x2_to_f32(x >> 8);
-                o[q] = make_float4(u.x * s, u.y * s, v.x * s, v.y * s);
+        for (int h = 0; h < kH8; ++h) acc[i][h][0] = acc[i][h][1] = 0;
+    const int qr = lane & 7, qh = 2 * (lane >> 3);   // scores: rows qr, qr + 8 and heads qh, qh + 1
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // (l: of this lane's rows)
+    for (; r0 < R; r0 += stride) {
+        const uint8_t* src = nxt;
+        nxt = row_at(r0 + stride + my);
+        const int nr = min(kSRows, R - r0);
+        float* o = rows + my * pitch;
+        const int nc = max(0, min(nr, nsel - r0));   // compressed ones of the rows
+        if (nc < nr) {
+            const uint8_t* w = wrows + (int64_t)(r0 + nc - nsel) * D * esz + 16 * lane;
+            int r = nc + wr0, c = wc0;
+            while (r < nr) {
+                if (a.q_dtype == LCS_F32) cp_async_16(rows + r * pitch + 4 * c, w, true);
+                else put_bf16x8(rows + r * pitch + 8 * c, __ldg(reinterpret_cast<const uint4*>(w)));
+                w += 512;
+                r += wrs, c += wcs;
+                if (c >= pieces) c -= pieces, ++r;
             }
+            cp_async_commit();
         }
-        for (int i = t; i < nc * a.d_r / 2; i += kSThreads) {
-            const int r = i / (a.d_r / 2), j = 2 * (i - r * (a.d_r / 2));
-            const uint8_t* src = ptr[k][r];
-            const uint32_t w = src != nullptr ? __ldg(reinterpret_cast<const uint32_t*>(src + a.d_c / 2 + 2 * j)) : 0u;
-            *reinterpret_cast<float2*>(rows + r * pitch + a.d_c + j) = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-        }
-        for (int i = t; i < (nr - nc) * (D / 4); i += kSThreads) {
-            const int r = nc + i / (D / 4), j = 4 * (i % (D / 4));
-            float4 v;
-            if (a.q_dtype == LCS_F32) v = __ldg(reinterpret_cast<const float4*>(ptr[k][r]) + j / 4);
-            else {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(ptr[k][r]) + j / 4);
-                v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                                __uint_as_float(w.y & 0xFFFF0000u));
-            }
-            *reinterpret_cast<float4*>(rows + r * pitch + j) = v;
-        }
-        __syncthreads();
-        {   // warp = head, lane = rows lane and lane + 32
-            float s[2] = {-INFINITY, -INFINITY};
-            if (warp < nh) {
-                const float4* q4 = reinterpret_cast<const float4*>(qs + warp * D);
-                const float4* ra = reinterpret_cast<const float4*>(rows + lane * pitch);
-                const float4* rb = reinterpret_cast<const float4*>(rows + (lane + 32) * pitch);
-                float sa = 0.f, sb = 0.f;   // (rows past nr hold anything: dropped below)
-#pragma unroll 4
-                for (int c = 0; c < D / 4; ++c) {
-                    const float4 q = q4[c];
-                    sa = dot4(q, ra[c], sa);
-                    if (nr > 32) sb = dot4(q, rb[c], sb);
+        if (my < nc) {
+            for (int c = half; c < a.d_c / 32; c += 2) {   // 32 codes and their scale
+                const uint4 w = src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+                const float s = src != nullptr ? e4m3_to_f32(__ldg(src + a.d_c / 2 + 2 * a.d_r + c)) : 0.f;
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t y = x[i >> 1] >> (16 * (i & 1));
+                    const float2 u = e2m1x2_to_f32(y), v = e2m1x2_to_f32(y >> 8);
+                    reinterpret_cast<float4*>(o + 32 * c)[i] = make_float4(u.x * s, u.y * s, v.x * s, v.y * s);
                 }
-                if (lane < nr) s[0] = sa * a.scale;
-                if (lane + 32 < nr) s[1] = sb * a.scale;
             }
-            const float mx = fmaxf(m, warp_max(fmaxf(s[0], s[1])));
-            const float alpha = m == -INFINITY ? 0.f : expf(m - mx);
-            const float p0 = s[0] == -INFINITY ? 0.f : expf(s[0] - mx), p1 = s[1] == -INFINITY ? 0.f : expf(s[1] - mx);
-            l = l * alpha + warp_sum(p0 + p1);
-            m = mx;
-            sc[warp * kSRows + lane] = p0;
-            sc[warp * kSRows + 32 + lane] = p1;
-            if (lane == 0) al[warp] = alpha;
+            for (int c = half; c < a.d_r / 8; c += 2)
+                put_bf16x8(o + a.d_c + 8 * c,
+                           src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src + a.d_c / 2) + c) : make_uint4(0, 0, 0, 0));
         }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int j = first + step * i;
-            if (j >= items) break;
-            const int h = j / c4n, c = j - h * c4n;
-            const float f = al[h];
-            float4 o = make_float4(acc[i].x * f, acc[i].y * f, acc[i].z * f, acc[i].w * f);
-            const float4* v4 = reinterpret_cast<const float4*>(rows + 4 * c);
+        cp_async_wait<0>();
+        __syncwarp();
+        float s[2][2];   // [row][head]
+        {
+            const ulonglong2* qa = reinterpret_cast<const ulonglong2*>(qs + qh * pitch);
+            const ulonglong2* qb = reinterpret_cast<const ulonglong2*>(qs + (qh + 1) * pitch);
+            const ulonglong2* ra = reinterpret_cast<const ulonglong2*>(rows + qr * pitch);
+            const ulonglong2* rb = reinterpret_cast<const ulonglong2*>(rows + (qr + 8) * pitch);
+            uint64_t s2[2][2] = {{0, 0}, {0, 0}};
 #pragma unroll 4
-            for (int r = part; r < nr; r += share) {
-                const float p = sc[h * kSRows + r];
-                const float4 v = v4[r * (pitch / 4)];
-                o = make_float4(fmaf(p, v.x, o.x), fmaf(p, v.y, o.y), fmaf(p, v.z, o.z), fmaf(p, v.w, o.w));
+            for (int c = 0; c < D / 4; ++c) {
+                const ulonglong2 u = qa[c], v = qb[c], x = ra[c], y = rb[c];
+                s2[0][0] = fma2(u.y, x.y, fma2(u.x, x.x, s2[0][0]));
+                s2[0][1] = fma2(v.y, x.y, fma2(v.x, x.x, s2[0][1]));
+                s2[1][0] = fma2(u.y, y.y, fma2(u.x, y.x, s2[1][0]));
+                s2[1][1] = fma2(v.y, y.y, fma2(v.x, y.x, s2[1][1]));
             }
-            acc[i] = o;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 v = unpack2(s2[r][h]);   // (rows past nr hold anything: dropped)
+                    s[r][h] = qr + 8 * r < nr ? (v.x + v.y) * a.scale : -INFINITY;
+                }
         }
-        __syncthreads();
+        float p[2][2], al[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float mx = fmaxf(s[0][h], s[1][h]);
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            mx = fmaxf(mx, m[h]);
+            al[h] = m[h] == -INFINITY ? 0.f : expf(m[h] - mx);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) p[r][h] = s[r][h] == -INFINITY ? 0.f : expf(s[r][h] - mx);
+            l[h] = fmaf(l[h], al[h], p[0][h] + p[1][h]);
+            m[h] = mx;
+        }
+        *reinterpret_cast<float2*>(wt + qr * kSHeads + qh) = make_float2(p[0][0], p[0][1]);
+        *reinterpret_cast<float2*>(wt + (qr + 8) * kSHeads + qh) = make_float2(p[1][0], p[1][1]);
+        if (qr == 0) *reinterpret_cast<float2*>(ml + qh) = make_float2(al[0], al[1]);
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < kH8; ++h) {
+            const uint64_t f = pack2(ml[grp * kH8 + h], ml[grp * kH8 + h]);
+#pragma unroll
+            for (int i = 0; i < kPass; ++i) acc[i][h][0] = mul2(acc[i][h][0], f), acc[i][h][1] = mul2(acc[i][h][1], f);
+        }
+#pragma unroll 2
+        for (int r = 0; r < nr; ++r) {
+            float w[kH8];
+            if constexpr (kH8 == 2) {
+                const float2 x = *reinterpret_cast<const float2*>(wt + r * kSHeads + 2 * grp);
+                w[0] = x.x, w[1] = x.y;
+            } else {
+#pragma unroll
+                for (int h = 0; h < kH8; h += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(wt + r * kSHeads + kH8 * grp + h);
+                    w[h] = x.x, w[h + 1] = x.y, w[h + 2] = x.z, w[h + 3] = x.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPass; ++i) {
+                const int c = col + kSpan * i;
+                if (c >= c4n) break;
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(rows + r * pitch + 4 * c);
+#pragma unroll
+                for (int h = 0; h < kH8; ++h) {
+                    const uint64_t p2 = pack2(w[h], w[h]);
+                    acc[i][h][0] = fma2(p2, v.x, acc[i][h][0]);
+                    acc[i][h][1] = fma2(p2, v.y, acc[i][h][1]);
+                }
+            }
+        }
+        __syncwarp();
     }
-    if (warp < nh && lane == 0) {
-        lh[warp] = l;
-        if (a.lse != nullptr) a.lse[g * a.H + h0 + warp] = l > 0.f ? m + logf(l) : -INFINITY;
+    // ---- the warps' partials: O [8, d_c] where their rows were, m and l
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
+        if (qr == 0) ml[qh + h] = m[h], ml[kSHeads + qh + h] = l[h];
+    }
+#pragma unroll
+    for (int i = 0; i < kPass; ++i) {
+        const int c = col + kSpan * i;
+        if (c >= c4n) break;
+#pragma unroll
+        for (int h = 0; h < kH8; ++h)
+            *reinterpret_cast<ulonglong2*>(rows + (grp * kH8 + h) * a.d_c + 4 * c) = make_ulonglong2(acc[i][h][0], acc[i][h][1]);
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int j = first + step * i;
-        float4 o = acc[i];
-        for (int d = 1; d < share; d <<= 1) {   // the threads that shared an item are neighbours in a warp
-            o.x += __shfl_xor_sync(0xffffffffu, o.x, d);
-            o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
-            o.z += __shfl_xor_sync(0xffffffffu, o.z, d);
-            o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+    // ---- joined over the CTA's warps and written, or (of several splits) left in the first warp's place
+    float* base = qs + kSHeads * pitch;
+    const int in_ml = kSRows * pitch + kSRows * kSHeads;   // of a warp's floats
+    auto out_at = [&](int h, int c, float4 o, float M, float L) {
+        const float iv = L > 0.f ? 1.f / L : 0.f;
+        o = scale4(o, iv);
+        const int64_t at = (g * a.H + h0 + h) * a.d_c + 4 * c;
+        if (a.out_dtype == LCS_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = o;
+        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(cvt_bf16x2(o.x, o.y), cvt_bf16x2(o.z, o.w));
+        if (c == 0 && a.lse != nullptr) a.lse[g * a.H + h0 + h] = L > 0.f ? M + logf(L) : -INFINITY;
+    };
+    for (int j = t; j < nh * c4n; j += blockDim.x) {
+        const int h = j / c4n, c = j - h * c4n;
+        float M = -INFINITY, L = 0.f;
+        for (int w = 0; w < nw; ++w) M = fmaxf(M, base[w * wf + in_ml + h]);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < nw; ++w) {
+            const float* x = base + w * wf;
+            const float lw = x[in_ml + kSHeads + h], f = lw > 0.f ? expf(x[in_ml + h] - M) : 0.f;
+            L = fmaf(lw, f, L);
+            o = axpy4(f, *reinterpret_cast<const float4*>(x + h * a.d_c + 4 * c), o);
         }
-        if (j >= items || part != 0) continue;
-        const int h = j / c4n;
-        const float iv = lh[h] > 0.f ? 1.f / lh[h] : 0.f;
-        const int64_t at = (g * a.H + h0) * a.d_c + 4 * j;
-        if (a.out_dtype == LCS_F32)
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
-        else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-                make_uint2(cvt_bf16x2(o.x * iv, o.y * iv), cvt_bf16x2(o.z * iv, o.w * iv));
+        if (splits == 1) out_at(h, c, o, M, L);
+        else {
+            *reinterpret_cast<float4*>(base + h * a.d_c + 4 * c) = o;
+            if (c == 0) joint[0][h] = M, joint[1][h] = L;
+        }
     }
+    if (splits == 1) return;
+    // ---- and over the cluster's CTAs, each a share of the outputs
+    __syncwarp();
+    cluster_sync_all();
+    for (int j = sp * blockDim.x + t; j < nh * c4n; j += splits * blockDim.x) {
+        const int h = j / c4n, c = j - h * c4n;
+        float M = -INFINITY, L = 0.f;
+        for (int s = 0; s < splits; ++s) M = fmaxf(M, ld_dsmem_f32(dsmem_addr(&joint[0][h], s)));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < splits; ++s) {
+            const float ls = ld_dsmem_f32(dsmem_addr(&joint[1][h], s));
+            const float f = ls > 0.f ? expf(ld_dsmem_f32(dsmem_addr(&joint[0][h], s)) - M) : 0.f;
+            L = fmaf(ls, f, L);
+            o = axpy4(f, ld_dsmem_f4(dsmem_addr(base + h * a.d_c + 4 * c, s)), o);
+        }
+        out_at(h, c, o, M, L);
+    }
+    __syncwarp();
+    cluster_sync_all();   // no CTA leaves while its partials are read
+}
+
+// Warps per CTA and splits (CTAs of a cluster) per query and group of heads: CTAs of four warps while
+// there are enough of them; few ones get eight warps, then up to eight splits, while every warp has rows.
+struct SimtPlan {
+    int warps, splits;
+    size_t smem;
+};
+SimtPlan simt_plan(const AttendKv4Args& a) {
+    const int D = a.d_c + a.d_r;
+    const int64_t most_w = a.q_pos == nullptr ? a.Tw : (a.W < a.Tw ? a.W : a.Tw);
+    const int64_t blocks = ((a.idx != nullptr ? a.k : a.max_blocks * a.be) + most_w + kSRows - 1) / kSRows;
+    const int64_t ctas = a.B * a.Q * ((a.H + kSHeads - 1) / kSHeads);
+    const size_t fixed = sizeof(float) * kSHeads * (D + 4), per = sizeof(float) * simt_warp_floats(D), most = 227 * 1024 - 1024;
+    SimtPlan p{ctas < num_sms() ? 8 : 4, 1, 0};
+    while (p.warps > 1 && (p.warps / 2 >= blocks || fixed + p.warps * per > most)) p.warps /= 2;
+    while (p.splits < kSMaxCluster && ctas * p.splits * 2 <= num_sms() && blocks > p.warps * p.splits) p.splits *= 2;
+    p.smem = fixed + p.warps * per;
+    return p;
+}
+
+template <int G, int kPass>
+cudaError_t launch_simt(const AttendKv4Args& a, int* status, cudaStream_t s) {
+    const SimtPlan p = simt_plan(a);
+    auto kern = attend_kv4_kernel<G, kPass>;
+    cudaError_t e = set_smem_here(reinterpret_cast<const void*>(kern), p.smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.B * a.Q), (unsigned)((a.H + kSHeads - 1) / kSHeads), (unsigned)p.splits);
+    cfg.blockDim = dim3((unsigned)p.warps * 32);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = (unsigned)p.splits;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a, p.splits, status);
 }
 
 // ----------------------------------------------------------- tensor-core path
@@ -1207,13 +1370,11 @@ cudaError_t launch_attend_kv4(const AttendKv4Args& a, void* scratch, int* status
     const int64_t queries = a.B * a.Q;
     if (queries == 0) return cudaSuccess;
     if (use_tc(a)) return launch_tc(a, scratch, status, s);
-    const int D = a.d_c + a.d_r;
-    const size_t smem = sizeof(float) * (kSHeads * D + kSRows * (D + 4) + kSHeads * kSRows);
-    auto kern = a.d_c <= 128 ? attend_kv4_kernel<kSHeads * 128 / 4 / kSThreads> : attend_kv4_kernel<kSHeads * kSMaxDc / 4 / kSThreads>;
-    cudaError_t e = set_smem_here(reinterpret_cast<const void*>(kern), smem);
-    if (e != cudaSuccess) return e;
-    return launch_k(kern, dim3((unsigned)queries, (unsigned)((a.H + kSHeads - 1) / kSHeads)), dim3(kSThreads), smem, s, false,
-                    a, status);
+    if (a.d_c <= 32) return launch_simt<4, 1>(a, status, s);
+    if (a.d_c <= 64) return launch_simt<2, 1>(a, status, s);
+    if (a.d_c <= 128) return launch_simt<1, 1>(a, status, s);
+    if (a.d_c <= 256) return launch_simt<1, 2>(a, status, s);
+    return launch_simt<1, 4>(a, status, s);
 }
 
 }  // namespace lcs
