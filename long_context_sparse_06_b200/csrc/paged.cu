@@ -3,6 +3,7 @@
 //
 // "DeepSeek V4 深度解析" §4 keeps the compressed cache in blocks that cover lcm(4, 128)
 // raw tokens; its FP4 paragraph gives the 4-bit format (E2M1 codes, an E4M3 scale per 32).
+#include <type_traits>
 #include <utility>
 
 #include "lcs_common.cuh"
@@ -191,13 +192,35 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // ---------------------------------------------------------- 4-bit rows: write, read
-// E2M1 code (magnitude bits) of |v| / sc without the division: |v| against the code grid's midpoints
-// times sc (0.25 .. 5 times an E4M3 value: exact, even in bf16).  Ties go to the even code, so the
-// midpoints below odd codes count to the code under them: a search of three steps, the first two with
-// >=, the last with >.  (A quotient rounded to fp32 meets a midpoint only when the exact one does:
-// a midpoint has 3 bits, a value within 2^-24 of it but not on it would need more than 24.)
-//
-// fp32 rows: 16 elements of a lane, eight codes a word.
+// E2M1 codes of v / sc without a division per element: v (r + rl) in one fused step, r the reciprocal
+// rounded down and rl what it lacks, is (v / sc)(1 + 2^-46) before its rounding to fp32.  The codes can
+// only differ from the quotient's at the code grid's midpoints, which have three bits: times sc
+// (four bits) they are fp32 values, so a v that is not one of them lies at least a step of its 24 bits
+// away, more than half a step of the quotient's; a v that is one gives the midpoint itself, which goes to
+// the even code.  (rl is not negative and not 0: -0 stays -0, an infinity infinite.)
+struct Recip {
+    uint64_t r, rl;   // in both halves
+};
+__device__ __forceinline__ Recip recip_of(float sc) {
+    const float r = __frcp_rd(sc), rl = fmaxf(fmaf(-r, sc, 1.f) * r, 1.17549435e-38f);
+    return {pack2(r, r), pack2(rl, rl)};
+}
+__device__ __forceinline__ float2 quotients(uint64_t v, const Recip& q) { return unpack2(fma2(v, q.r, mul2(v, q.rl))); }
+// Eight floats -> eight E2M1 codes, low nibble first, saturating.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(float2 a, float2 b, float2 c, float2 d) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+    return r;
+}
+
+// 16 elements of a lane, fp32 ...
 struct LaneF32 {
     float4 v[4];
     __device__ __forceinline__ void load(const float* p) {
@@ -214,22 +237,20 @@ struct LaneF32 {
         for (int i = 0; i < 4; ++i) m = fmaxf(fmaxf(m, fmaxf(fabsf(v[i].x), fabsf(v[i].y))), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
         return m;
     }
+    static __device__ __forceinline__ float sixth(float amax) { return amax / 6.0f; }
     __device__ __forceinline__ uint2 codes(float sc) const {
-        const float t0 = 0.25f * sc, t1 = 0.75f * sc, t2 = 1.25f * sc, t3 = 1.75f * sc, t4 = 2.5f * sc, t5 = 3.5f * sc, t6 = 5.f * sc;
-        uint32_t w[2] = {0, 0};
+        const Recip q = recip_of(sc);
+        uint32_t w[2];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float x = i & 2 ? (i & 1 ? v[i >> 2].w : v[i >> 2].z) : (i & 1 ? v[i >> 2].y : v[i >> 2].x);
-            const float a = fabsf(x);
-            const bool p1 = a >= t3, p2 = a >= (p1 ? t5 : t1);
-            const bool p3 = a > (p1 ? (p2 ? t6 : t4) : (p2 ? t2 : t0));
-            const uint32_t c = (p1 ? 4u : 0u) + (p2 ? 2u : 0u) + (p3 ? 1u : 0u) + ((__float_as_uint(x) >> 28) & 8u);
-            w[i >> 3] |= c << (4 * (i & 7));
+        for (int h = 0; h < 2; ++h) {
+            const float4 a = v[2 * h], b = v[2 * h + 1];
+            w[h] = cvt_e2m1x8(quotients(pack2(a.x, a.y), q), quotients(pack2(a.z, a.w), q), quotients(pack2(b.x, b.y), q),
+                              quotients(pack2(b.z, b.w), q));
         }
         return make_uint2(w[0], w[1]);
     }
 };
-// bf16 rows: two elements an instruction.
+// ... and bf16.
 struct LaneBf16 {
     uint4 v[2];
     __device__ __forceinline__ void load(const __nv_bfloat16* p) {
@@ -237,56 +258,52 @@ struct LaneBf16 {
         for (int i = 0; i < 2; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
     }
     __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ uint32_t word(int i) const {
-        const uint4 x = v[i >> 2];
-        return i & 2 ? (i & 1 ? x.w : x.z) : (i & 1 ? x.y : x.x);
-    }
-    static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
     __device__ __forceinline__ float amax() const {
-        __nv_bfloat162 m = two(0u);
+        uint32_t m = 0;   // (a NaN loses)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = __hmax2(m, two(word(i) & 0x7FFF7FFFu));   // (a NaN loses)
-        return fmaxf(__low2float(m), __high2float(m));
+        for (int i = 0; i < 2; ++i)
+            m = bf16x2_maxabs(bf16x2_maxabs(bf16x2_maxabs(m, v[i].x), bf16x2_maxabs(v[i].y, v[i].z)), v[i].w);
+        return fmaxf(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xFFFF0000u)));
     }
+    // (for every amax of 8 bits the product has the E4M3 value of the quotient: all of them compared on the host)
+    static __device__ __forceinline__ float sixth(float amax) { return amax * (1.0f / 6.0f); }
     __device__ __forceinline__ uint2 codes(float sc) const {
-        uint32_t t[7];
-        constexpr float mid[7] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.f};
+        const Recip q = recip_of(sc);
+        auto two = [&](uint32_t w) { return quotients(pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), q); };
+        uint32_t w[2];
 #pragma unroll
-        for (int k = 0; k < 7; ++k) t[k] = cvt_bf16x2(mid[k] * sc, mid[k] * sc);
-        uint32_t w[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t x = word(i);
-            const __nv_bfloat162 a = two(x & 0x7FFF7FFFu);
-            const uint32_t m1 = __hge2_mask(a, two(t[3]));
-            const uint32_t m2 = __hge2_mask(a, two((m1 & t[5]) | (~m1 & t[1])));
-            const uint32_t hi = (m2 & t[6]) | (~m2 & t[4]), lo = (m2 & t[2]) | (~m2 & t[0]);
-            const uint32_t m3 = __hgt2_mask(a, two((m1 & hi) | (~m1 & lo)));
-            uint32_t c = (m1 & 0x00040004u) | (m2 & 0x00020002u);
-            c |= (m3 & 0x00010001u) | ((x >> 12) & 0x00080008u);
-            w[i >> 2] |= ((c | (c >> 12)) & 0xFFu) << (8 * (i & 3));   // element 2j in the low nibble
-        }
+        for (int h = 0; h < 2; ++h) w[h] = cvt_e2m1x8(two(v[h].x), two(v[h].y), two(v[h].z), two(v[h].w));
         return make_uint2(w[0], w[1]);
     }
 };
 __device__ __forceinline__ uint16_t to_bf16_bits(float v) { return f32_to_bf16_bits(v); }
 __device__ __forceinline__ uint16_t to_bf16_bits(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 
-// One warp takes kRowsFly rows at a time, their loads in flight together; two lanes share a 32-element
-// block, 16 elements each: the block's amax is one shuffle, a lane's codes one 8-byte store.  Bound by HBM:
-// 1152 or 2304 bytes read and 400 written a row.
-constexpr int kRowsFly = 2, kRowsCtas = 5;   // CTAs per SM (262144 bf16 rows stored and read: 211 us; 1 x 6: 235, 4 x 4: 219)
+// One warp takes kRowsFly rows at a time, their loads in flight together and the next slots on their way;
+// two lanes share a 32-element block, 16 elements each: the block's amax is one shuffle, a lane's codes
+// one 8-byte store.  Bound by HBM: 1152 or 2304 bytes read and 400 written a row.  262144 rows, us (at the
+// measured copy rate): bf16 stored 82 (63), loaded 76 (63); fp32 stored 121 (110), loaded 131 (110).  With
+// seven thresholds per element in place of the quotient, and slots asked for when they are needed, the
+// stores took 127 and 174.  bf16 stored and loaded, by rows in flight x CTAs per SM: 162 (2 x 5), 170
+// (2 x 6), 172 (4 x 4).
+constexpr int kRowsFly = 2;
+template <typename T>
+constexpr int rows_ctas() {   // CTAs per SM: what the registers allow
+    return sizeof(T) == 4 ? 4 : 5;
+}
 template <typename T, typename Lane>
-__global__ void __launch_bounds__(256, kRowsCtas) kv4_store_kernel(const T* __restrict__ x, const int64_t* __restrict__ slots,
+__global__ void __launch_bounds__(256, rows_ctas<T>()) kv4_store_kernel(const T* __restrict__ x, const int64_t* __restrict__ slots,
                                                         int64_t n, int d_c, int d_r, int row_bytes,
                                                         uint8_t* __restrict__ pool, int64_t n_slots, int fly, int* status) {
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5), w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int D = d_c + d_r;
+    int64_t next = lane < fly && w * fly + lane < n ? __ldg(slots + w * fly + lane) : -1;
     for (int64_t r0 = w * fly; r0 < n; r0 += warps * fly) {
-        int64_t mine = -1;
+        int64_t mine = next;
+        next = -1;
         if (lane < fly && r0 + lane < n) {
-            mine = __ldg(slots + r0 + lane);
+            if (r0 + warps * fly + lane < n) next = __ldg(slots + r0 + warps * fly + lane);   // (on its way meanwhile)
             if (mine >= n_slots) {
                 set_status(status, LCS_ERR_DEVICE, 502);
                 mine = -1;
@@ -309,7 +326,7 @@ __global__ void __launch_bounds__(256, kRowsCtas) kv4_store_kernel(const T* __re
                 float amax = v[u].amax();
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 if (!in || slot[u] < 0) continue;
-                uint8_t sc_code = f32_to_e4m3(amax / 6.0f);
+                uint8_t sc_code = f32_to_e4m3(Lane::sixth(amax));
                 if ((sc_code & 0x7F) == 0) sc_code = 0x38;   // 1.0
                 uint8_t* o = pool + slot[u] * row_bytes;
                 *reinterpret_cast<uint2*>(o + 8 * p) = v[u].codes(e4m3_to_f32(sc_code));
@@ -329,16 +346,15 @@ __global__ void __launch_bounds__(256, kRowsCtas) kv4_store_kernel(const T* __re
     }
 }
 
-// 16 values of a lane: eight packed codes a word, times the scale.
-__device__ __forceinline__ void store16(float* o, uint2 c, float sc) {
+// A lane's 32 bytes of a row: 8 fp32 or 16 bf16 values, eight packed codes a word, times the scale.
+__device__ __forceinline__ void store_lane(float* o, uint32_t c, float sc) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t w = (i < 2 ? c.x : c.y) >> (16 * (i & 1));
-        const float2 a = e2m1x2_to_f32(w), b = e2m1x2_to_f32(w >> 8);
+    for (int i = 0; i < 2; ++i) {
+        const float2 a = e2m1x2_to_f32(c >> (16 * i)), b = e2m1x2_to_f32(c >> (16 * i + 8));
         reinterpret_cast<float4*>(o)[i] = make_float4(a.x * sc, a.y * sc, b.x * sc, b.y * sc);
     }
 }
-__device__ __forceinline__ void store16(__nv_bfloat16* o, uint2 c, float sc) {
+__device__ __forceinline__ void store_lane(__nv_bfloat16* o, uint2 c, float sc) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t w = i ? c.y : c.x;
@@ -354,38 +370,42 @@ __device__ __forceinline__ void store16(__nv_bfloat16* o, uint2 c, float sc) {
 
 // The same split of the work: code x scale is exact in bf16 (six significant bits), the RoPE dims are bf16.
 template <typename T>
-__global__ void __launch_bounds__(256, kRowsCtas) kv4_load_kernel(const uint8_t* __restrict__ pool, int64_t n_slots,
+__global__ void __launch_bounds__(256, rows_ctas<T>()) kv4_load_kernel(const uint8_t* __restrict__ pool, int64_t n_slots,
                                                        const int64_t* __restrict__ slots, int64_t n, int d_c, int d_r,
                                                        int row_bytes, T* __restrict__ out, int fly, int* status) {
+    using Codes = typename std::conditional<sizeof(T) == 4, uint32_t, uint2>::type;
+    constexpr int kDims = 32 / sizeof(T);
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5), w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int D = d_c + d_r;
+    int64_t next = lane < fly && w * fly + lane < n ? __ldg(slots + w * fly + lane) : -2;
     for (int64_t r0 = w * fly; r0 < n; r0 += warps * fly) {
         int64_t mine = -2;                       // past the last row
         if (lane < fly && r0 + lane < n) {
-            mine = __ldg(slots + r0 + lane);
+            mine = next;
+            if (r0 + warps * fly + lane < n) next = __ldg(slots + r0 + warps * fly + lane);
             if (mine >= n_slots) set_status(status, LCS_ERR_DEVICE, 503);
             if (mine < 0 || mine >= n_slots) mine = -1;   // a row of zeros
         }
         int64_t slot[kRowsFly];
 #pragma unroll
         for (int u = 0; u < kRowsFly; ++u) slot[u] = __shfl_sync(0xffffffffu, mine, u);
-        for (int p = lane; p < d_c / 16; p += 32) {
-            uint2 c[kRowsFly];
+        for (int p = lane; p < d_c / kDims; p += 32) {
+            Codes c[kRowsFly];
             uint8_t sb[kRowsFly];
 #pragma unroll
             for (int u = 0; u < kRowsFly; ++u) {
-                c[u] = make_uint2(0, 0);
+                c[u] = Codes{};
                 sb[u] = 0;
                 if (slot[u] >= 0) {
                     const uint8_t* src = pool + slot[u] * row_bytes;
-                    c[u] = __ldg(reinterpret_cast<const uint2*>(src + 8 * p));
-                    sb[u] = __ldg(src + d_c / 2 + 2 * d_r + p / 2);
+                    c[u] = __ldg(reinterpret_cast<const Codes*>(src) + p);
+                    sb[u] = __ldg(src + d_c / 2 + 2 * d_r + p / (32 / kDims));
                 }
             }
 #pragma unroll
             for (int u = 0; u < kRowsFly; ++u)
-                if (slot[u] > -2) store16(out + (r0 + u) * D + 16 * p, c[u], e4m3_to_f32(sb[u]));
+                if (slot[u] > -2) store_lane(out + (r0 + u) * D + kDims * p, c[u], e4m3_to_f32(sb[u]));
         }
         for (int j = 2 * lane; j < d_r; j += 64) {
             uint32_t h[kRowsFly];
@@ -410,8 +430,8 @@ struct RowsPlan {
     int fly;
     unsigned ctas;
 };
-RowsPlan rows_plan(int64_t n) {
-    const int64_t most = (int64_t)num_sms() * kRowsCtas;   // CTAs of 8 warps, all resident
+RowsPlan rows_plan(int64_t n, int per_sm) {
+    const int64_t most = (int64_t)num_sms() * per_sm;   // CTAs of 8 warps, all resident
     int fly = 1;
     while (fly < kRowsFly && n > most * 8 * fly) fly *= 2;
     const int64_t ctas = (n + 8 * fly - 1) / (8 * fly);
@@ -446,7 +466,7 @@ cudaError_t launch_kv4_store(const void* x, int x_dtype, int64_t n, int d_c, int
                              int64_t n_slots, int* status, cudaStream_t s) {
     if (n == 0) return cudaSuccess;
     const int rb = kv4_row_bytes(d_c, d_r);
-    const RowsPlan rp = rows_plan(n);
+    const RowsPlan rp = rows_plan(n, x_dtype == LCS_F32 ? rows_ctas<float>() : rows_ctas<__nv_bfloat16>());
     if (x_dtype == LCS_F32)
         return launch_k(kv4_store_kernel<float, LaneF32>, dim3(rp.ctas), dim3(256), 0, s, false,
                         static_cast<const float*>(x), slots, n, d_c, d_r, rb, static_cast<uint8_t*>(pool), n_slots,
@@ -460,7 +480,7 @@ cudaError_t launch_kv4_load(const void* pool, int64_t n_slots, const int64_t* sl
                             void* out, int out_dtype, int* status, cudaStream_t s) {
     if (n == 0) return cudaSuccess;
     const int rb = kv4_row_bytes(d_c, d_r);
-    const RowsPlan rp = rows_plan(n);
+    const RowsPlan rp = rows_plan(n, out_dtype == LCS_F32 ? rows_ctas<float>() : rows_ctas<__nv_bfloat16>());
     if (out_dtype == LCS_F32)
         return launch_k(kv4_load_kernel<float>, dim3(rp.ctas), dim3(256), 0, s, false,
                         static_cast<const uint8_t*>(pool), n_slots, slots, n, d_c, d_r, rb, static_cast<float*>(out),

@@ -341,6 +341,39 @@ def test_rows_equal_the_fp4_quantiser(G, orc, d_c, d_r, kind, dt):
 
 
 @gpu
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_rows_at_the_code_grids_midpoints(G, dt):
+    """Every scale with every midpoint times it and the values one step of the type beside it, signed zeros and
+    infinities: the quotient's codes (zeros keep their sign, infinities saturate with theirs)."""
+    scales = torch.tensor([(c & 7) * 2.0 ** -9 if c < 8 else (1 + (c & 7) / 8) * 2.0 ** ((c >> 3) - 7) for c in range(1, 127)])
+    mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    at = scales[:, None] * mids                                        # exact in either type
+    ints = torch.int32 if dt == torch.float32 else torch.int16
+    step = lambda d: (at.to(dt).view(ints) + d).view(dt).float()
+    x = torch.cat((step(-1), at, step(1), -at, 6 * scales[:, None], 0 * at[:, :2], -0.0 * at[:, :1]), 1)
+    x = torch.cat((x, 0 * x[:, :32 - x.shape[1]] if x.shape[1] < 32 else x[:, :0]), 1)[:, :32].contiguous()
+    x[:, 28] = 6 * scales                                              # the block's largest: its scale is the one meant
+    x = torch.cat((x, x[:1].clone()))
+    x[-1, ::2], x[-1, 1::2] = math.inf, -math.inf
+    assert torch.equal(x, x.to(dt).float())
+    pool = torch.zeros((127, G.kv_fp4_row_bytes(32, 0)), dtype=torch.uint8, device=DEV)
+    G.lcs_kv4_store(x.to(dt).to(DEV), torch.arange(127, device=DEV), pool, d_c=32)
+    got = pool.cpu()
+    want_scale = torch.arange(1, 127, dtype=torch.uint8)
+    assert torch.equal(got[:126, 16], want_scale)
+    q = (x[:126].double() / scales[:, None].double())
+    grid = torch.tensor(LUT, dtype=torch.float64)
+    a = q.abs()
+    lo = (torch.bucketize(a, grid, right=True) - 1).clamp(0, 7)
+    hi = (lo + 1).clamp(max=7)
+    mid = (grid[lo] + grid[hi]) / 2
+    code = torch.where((a > mid) | ((a == mid) & (lo % 2 == 1)), hi, lo) + 8 * torch.signbit(q).long()
+    codes = torch.stack((got[:, :16] & 15, got[:, :16] >> 4), -1).view(127, 32)
+    assert torch.equal(codes[:126].long(), code)
+    assert codes[126].tolist() == [7, 15] * 16 and got[126, 16] == 126
+
+
+@gpu
 @pytest.mark.parametrize("n", [0, 1, 2, 9, 1000, 20011])
 def test_rows_any_count_and_bad_slots(G, n):
     x = torch.randn((n, 576), generator=gen(n), device=DEV)
