@@ -15,9 +15,43 @@ namespace lcs {
 
 namespace {
 
-// Entries of request b that exist: n_entries[b], within what the table can hold.
-__device__ __forceinline__ int64_t kv4_entries(const AttendKv4Args& a, int64_t b, int* status) {
-    int64_t n = a.n_entries[b];
+// Loads that stay where they are written: a plain __ldg may be moved down to its first use, behind the
+// barriers and waits that it should have run under.
+__device__ __forceinline__ int64_t ld_now(const int64_t* p) {
+    int64_t v;
+    asm volatile("ld.global.nc.s64 %0, [%1];" : "=l"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int32_t ld_now(const int32_t* p) {
+    int32_t v;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_now(const uint2* p) {
+    uint2 v;
+    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_now(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// What query g of request b is told about its rows: loads that depend on nothing, asked for together.
+struct Kv4Query {
+    int64_t n, pos, win;   // n_entries; q_pos; win_pos0 (causal) or n_win
+};
+__device__ __forceinline__ Kv4Query kv4_query(const AttendKv4Args& a, int64_t g, int64_t b) {
+    Kv4Query x{ld_now(a.n_entries + b), 0, a.Tw};
+    if (a.q_pos != nullptr) x.pos = ld_now(a.q_pos + g), x.win = ld_now(a.win_pos0 + b);
+    else if (a.n_win != nullptr) x.win = ld_now(a.n_win + b);
+    return x;
+}
+
+// Entries of the request that exist: n_entries, within what the table can hold.
+__device__ __forceinline__ int64_t kv4_entries(const AttendKv4Args& a, const Kv4Query& x, int* status) {
+    int64_t n = x.n;
     const int64_t most = a.max_blocks * a.be;
     if (n > most) {
         set_status(status, LCS_ERR_DEVICE, 601);
@@ -26,29 +60,24 @@ __device__ __forceinline__ int64_t kv4_entries(const AttendKv4Args& a, int64_t b
     return n < 0 ? 0 : n;
 }
 
-// Entries that HCA query g attends.
-__device__ __forceinline__ int64_t kv4_avail(const AttendKv4Args& a, int64_t g, int64_t n) {
+// Entries that an HCA query attends.
+__device__ __forceinline__ int64_t kv4_avail(const AttendKv4Args& a, const Kv4Query& x, int64_t n) {
     if (a.q_pos == nullptr) return n;
-    const int64_t p = a.q_pos[g];
-    const int64_t av = p < 0 ? 0 : (p < INT64_MAX ? p + 1 : p) / a.m;   // (no sum past 64 bits)
+    const int64_t p = x.pos < 0 ? 0 : (x.pos < INT64_MAX ? x.pos + 1 : x.pos);   // (no sum past 64 bits)
+    // nearly always of 32 bits, where the division is several times cheaper
+    const int64_t av = (p >> 31) == 0 ? (int64_t)((uint32_t)p / (uint32_t)a.m) : p / a.m;
     return av < n ? av : n;
 }
 
 struct Kv4Window {
     int64_t lo, n;
 };
-__device__ __forceinline__ Kv4Window kv4_window(const AttendKv4Args& a, int64_t g, int64_t b) {
-    Kv4Window w{0, a.Tw};
-    if (a.q_pos == nullptr) {
-        if (a.n_win != nullptr) {
-            const int64_t n = a.n_win[b];
-            w.n = n < 0 ? 0 : (n < a.Tw ? n : a.Tw);
-        }
-        return w;
-    }
+__device__ __forceinline__ Kv4Window kv4_window(const AttendKv4Args& a, const Kv4Query& x) {
+    Kv4Window w{0, x.win < 0 ? 0 : (x.win < a.Tw ? x.win : a.Tw)};
+    if (a.q_pos == nullptr) return w;
     // the query's own row, counted from the window's first (a difference past 64 bits is of no window row
     // either way)
-    int64_t hi = (int64_t)((uint64_t)a.q_pos[g] - (uint64_t)a.win_pos0[b]);
+    int64_t hi = (int64_t)((uint64_t)x.pos - (uint64_t)x.win);
     int64_t lo = hi < 0 ? 0 : hi - a.W + 1;
     if (lo < 0) lo = 0;
     if (hi > a.Tw - 1) hi = a.Tw - 1;
@@ -113,6 +142,7 @@ __global__ void __launch_bounds__(256, kPass == 1 ? 4 : 1) attend_kv4_kernel(con
     __shared__ float joint[2][kSHeads];          // this CTA's m and l
     const int64_t g = blockIdx.x, b = g / a.Q;
     const int h0 = blockIdx.y * kSHeads, nh = min(kSHeads, a.H - h0), sp = blockIdx.z;
+    const Kv4Query x = kv4_query(a, g, b);
 
     for (int i = t; i < kSHeads * (D / 8); i += blockDim.x) {
         const int h = i / (D / 8), c = i - h * (D / 8);
@@ -128,9 +158,9 @@ __global__ void __launch_bounds__(256, kPass == 1 ? 4 : 1) attend_kv4_kernel(con
             put_bf16x8(o, __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at)));
         }
     }
-    const int64_t n = kv4_entries(a, b, status);
+    const int64_t n = kv4_entries(a, x, status);
     const int32_t* sel = a.idx != nullptr ? a.idx + g * a.k : nullptr;
-    if (t == 0) nsel_s = sel != nullptr ? a.k : (int)kv4_avail(a, g, n);
+    if (t == 0) nsel_s = sel != nullptr ? a.k : (int)kv4_avail(a, x, n);
     __syncthreads();
     if (sel != nullptr) {
         int bad = a.k;
@@ -144,7 +174,7 @@ __global__ void __launch_bounds__(256, kPass == 1 ? 4 : 1) attend_kv4_kernel(con
     __syncthreads();
     const int nsel = nsel_s;
     if (sel != nullptr && t == 0 && nsel < a.k && sel[nsel] >= 0) set_status(status, LCS_ERR_DEVICE, 603);
-    const Kv4Window win = kv4_window(a, g, b);
+    const Kv4Window win = kv4_window(a, x);
     const int R = nsel + (int)win.n;
     const int my = lane & 15, half = lane >> 4;   // this lane's row of a block, and every other piece of it
     // window rows lie one after the other: pieces of 16 bytes of them, lane + 32 i: row and column
@@ -413,14 +443,25 @@ cudaError_t launch_simt(const AttendKv4Args& a, int* status, cudaStream_t s) {
 //    different chunks run side by side (two stages of 64 rows took 3400 cycles per 64 rows, where
 //    each step was the others' wait).
 //  * Warps 4-9 fill the even chunks, warps 10-15 the odd ones: a warp owns 8 rows and holds its next
-//    chunk's 400-byte rows in registers (seven 16-byte loads a lane), which then have two chunks'
-//    time to arrive (one group alone waited 1500 cycles for them, chunk after chunk).
+//    chunk's 400-byte rows in registers (seven loads a lane), which then have two chunks' time to
+//    arrive (one group alone waited 1500 cycles for them, chunk after chunk).  Three of four words of
+//    codes are widened by conversions, one by byte permutes (half and half: 279 against 287 us for 1000
+//    queries).
 //  * Warps 16 and 17 issue the MMAs with the whole warp in step and an elected lane's predicate on
 //    the instruction: 35 cycles per M = 64, N = 64 MMA alone on the SM (32 is its rate), where
 //    issue from a branch of one thread took 55 to 72.
-//  * Warps 0-3 bring in Q and run the online softmax (fp32, exp2).  Weights are kept 2^6 above 1, so
-//    that fp16 reaches down to 2^-31 of the largest; O is rescaled when a head's maximum grows by
-//    more than 2^8.
+//  * Q's tile of rows comes in as one bulk copy; every warp but the first group of producers, which
+//    fills the first chunk meanwhile, converts it and moves its TMEM part (12 warps: three per quarter of
+//    TMEM's lanes).
+//  * Warps 0-3 run the online softmax (fp32, exp2).  Weights are kept 2^6 above 1, so that fp16
+//    reaches down to 2^-31 of the largest; O is rescaled when a head's maximum grows by more than 2^8.
+//
+// What a CTA takes, in cycles (hca, 1000 causal queries of 64 heads, 24 chunks each; 267 us in all): 860
+// until TMEM is there, 3000 until Q and the row counts are, 4700 for Q's conversion beside the first
+// chunk's widening, 1100 into TMEM, 2000 to the first S, 2150 a chunk (its MMAs alone: 1680 at M = 64,
+// half the rate of M = 128, which O's 512 columns leave no TMEM for), 4900 for the rest.  csa, 1500 causal
+// queries over 1024 selected rows: 2400 a chunk, its rows scattered; 467 us.  Decode steps: 16 x 8320
+// rows 37.6 us, 32 x 640 19.4, one x 8320 19.5, 4 x 1152 15.6, one of 160 rows 13.0.
 constexpr int kH = 64, kD = 576, kDv = 512, kChunk = 48, kStages = 3;
 constexpr int kBlk = kChunk * 128;            // one SW128 column block of a chunk: 48 rows x 128 B
 constexpr int kStageBytes = 9 * kBlk;         // 54 KB
@@ -441,7 +482,9 @@ constexpr int kMaxSplits = 64, kMaxCluster = 16;
 constexpr int kOPitchF32 = kDv * 4 + 16;      // staged O rows (padded)
 constexpr int kOPitchBF16 = kDv * 2 + 16;
 static_assert(kH * kOPitchF32 <= kStages * kStageBytes, "staged O fits in the stages");
-static_assert(kTQ / 64 * kQBlk <= kStageBytes && kH * 128 == kQBlk, "Q's TMEM part passes through the last stage");
+// Q comes in as it is over stages 1 and 2; what goes to TMEM passes through the end of the stages and P.
+constexpr int kQRawBytes = kH * kD * 2, kQPassAt = kStages * kStageBytes + 2 * kPBytes - kTQ / 64 * kQBlk;
+static_assert(kStageBytes + kQRawBytes <= kQPassAt && kQPassAt >= 2 * kStageBytes && kQPassAt % 1024 == 0, "and stage 0 is free");
 // TMEM columns: O, S (even chunks in lanes 0-15 of each 32, odd ones in lanes 16-31), Q (twice, for
 // both halves of the lanes).
 constexpr uint32_t kTmS = 256, kTmQ = kTmS + kChunk, kHi16 = 16u << 16;
@@ -456,7 +499,7 @@ struct TcBars {
     uint64_t pfull[2];
     uint64_t ofull[2];                        // P.V of the chunk done
     uint64_t odone;                           // every P.V of this CTA done
-    uint64_t qfull;                           // Q is where the MMAs read it
+    uint64_t qraw, qfull;                     // Q has come in; Q is where the MMAs read it
     uint32_t tmem_base;
     int first_bad[kTcWarps];
     float qscale[kH];                         // 2^-e of head h: the true q is the stored one times it
@@ -521,7 +564,7 @@ __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int where) {
+__device__ __noinline__ bool warp_wait_on(uint64_t* bar, uint32_t parity, int* status, int where) {
     uint64_t t0 = 0;
     for (uint32_t polls = 1;; ++polls) {
         if (__all_sync(0xffffffffu, mbar_sleep(bar, parity))) return true;
@@ -534,6 +577,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* s
     }
 }
 
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int where) {
+    if (__all_sync(0xffffffffu, mbar_sleep(bar, parity))) return true;
+    return warp_wait_on(bar, parity, status, where);
+}
 __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -679,8 +726,11 @@ __device__ __forceinline__ void merge_task(const AttendKv4Args& a, int tiles, in
         a.lse[(int64_t)g * a.H + head] = L > 0.f ? (M + log2f(L)) / kLog2e : -INFINITY;
 }
 
+// kCsa: a selection (else every entry).  kJoin: the splits of a unit are a cluster and merge in it.  (Four
+// kernels and not one: what a CTA runs once comes cold from beyond the SM's instruction cache.)
+template <bool kCsa, bool kJoin>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    attend_kv4_tc_kernel(const AttendKv4Args a, int tiles, int splits, int clustered, float* __restrict__ part_o,
+    attend_kv4_tc_kernel(const AttendKv4Args a, int tiles, int splits, float* __restrict__ part_o,
                          float* __restrict__ part_ml, int* status) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ TcBars bars;
@@ -716,7 +766,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&bars.ofull[i], 1);
         }
         mbar_init(&bars.odone, 1);
-        mbar_init(&bars.qfull, kSoftWarps);
+        mbar_init(&bars.qraw, 1);
+        mbar_init(&bars.qfull, kQWarps);
         fence_barrier_init();
     }
     if (warp == kWarpQK) {
@@ -730,69 +781,86 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #if defined(__CUDA_ARCH__)
     asm volatile("griddepcontrol.wait;" ::: "memory");   // everything above reads no memory of the call
 #endif
-    // column block k of Q: the first ones pass through the last stage into TMEM
-    auto q_block = [&](int k) { return k < kTQ / 64 ? stage_s + (kStages - 1) * kStageBytes + k * kQBlk : q_s + (k - kTQ / 64) * kQBlk; };
-    // ---- the loads that nothing waits for, before everything else: Q as it is, in the SW128 layout ...
-    // (by every warp but the first group of producers, which fills the first chunk meanwhile)
+    // column block k of Q, 16-byte pieces of it as it came in
+    auto q_block = [&](int k) { return k < kTQ / 64 ? stage_s + kQPassAt + k * kQBlk : q_s + (k - kTQ / 64) * kQBlk; };
+    const uint4* q_raw = reinterpret_cast<const uint4*>(stage_s + kStageBytes);
+    // Q is converted by every warp but the first group of producers, which fills the first chunk meanwhile
     const bool q_warp = !producer || pg != 0;
     const int q_id = warp < kSoftWarps ? warp : warp - kProdWarps;   // 0 .. kQWarps - 1
-    if (q_warp) {
-        const uint8_t* qg = static_cast<const uint8_t*>(a.q) + ((int64_t)g * a.H + h0) * (kD * 2);
-#pragma unroll 4
-        for (int i = q_id * 32 + lane; i < kH * 72; i += kQWarps * 32) {
-            const int h = i / 72, c = i - h * 72;
-            cp_async_16(q_block(c >> 3) + sw128_off(h, c & 7), qg + (h < nh ? i * 16 : 0), h < nh);
-        }
-        cp_async_commit();
+    // ---- the loads that nothing waits for, before everything else: Q, a tile of rows in one piece ...
+    if (threadIdx.x == 0) {
+        mbar_arrive_expect_tx(&bars.qraw, (uint32_t)(nh * kD * 2));
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(q_raw)),
+                     "l"(static_cast<const uint8_t*>(a.q) + ((int64_t)g * a.H + h0) * (kD * 2)), "r"(nh * kD * 2), "r"(smem_u32(&bars.qraw))
+                     : "memory");
     }
-    // ... and the producers' first rows.  A group takes every other chunk.  How many entries there are, and
-    // which of a chunk's rows are attended (the selection's length), is known later: rows past it
-    // are dropped when they are widened.
-    const int32_t* sel = a.idx != nullptr ? a.idx + (int64_t)g * a.k : nullptr;
+    const Kv4Query x = kv4_query(a, g, b);
+    // ... the selection (CSA), of which the valid prefix counts, and the producers' first two rows: a group takes
+    // every other chunk.  How many entries there are, and which of a chunk's rows are attended (the
+    // selection's length), is known later: rows past it are dropped when they are widened.
+    const int32_t* sel = kCsa ? a.idx + (int64_t)g * a.k : nullptr;
     const int held = (int)(a.max_blocks * a.be);   // entries that the table can hold
     auto gcof = [&](int c) -> int { return sp + splits * c; };
     const int my_row = pw * kRowsPerWarp + lane % kRowsPerWarp, my_piece = lane / kRowsPerWarp;
+    int e0 = -1, e1 = -1, seen[2] = {0, 0};
+    if (producer) {
+        const int j0 = gcof(pg) * kChunk + my_row, j1 = gcof(pg + kProdGroups) * kChunk + my_row, lim = kCsa ? a.k : held;
+        if (j0 < lim) e0 = kCsa ? ld_now(sel + j0) : j0;
+        if (j1 < lim) e1 = kCsa ? ld_now(sel + j1) : j1;
+    }
+    if (kCsa) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if ((int)threadIdx.x + i * kTcThreads < a.k) seen[i] = ld_now(sel + threadIdx.x + i * kTcThreads);
+    }
+    const bool in0 = e0 >= 0 && e0 < held, in1 = e1 >= 0 && e1 < held;
+    const int b0 = in0 ? e0 / a.be : 0, b1 = in1 ? e1 / a.be : 0;
+    const int32_t id0 = in0 ? ld_now(a.table + (int64_t)b * a.max_blocks + b0) : -1;
+    const int32_t id1 = in1 ? ld_now(a.table + (int64_t)b * a.max_blocks + b1) : -1;
     auto row_of = [&](int c, int lim) -> const uint8_t* {   // this lane's row of local chunk c, null if there is none
         const int j = gcof(c) * kChunk + my_row;
-        if (j >= (sel != nullptr ? a.k : lim)) return nullptr;
-        const int e = sel != nullptr ? __ldg(sel + j) : j;
+        if (j >= (kCsa ? a.k : lim)) return nullptr;
+        const int e = kCsa ? __ldg(sel + j) : j;
         return e >= 0 && e < lim ? kv4_row(a, b, e) : nullptr;
     };
     RawRow raw;
     auto load_half = [&](const uint8_t* src, int hf) {
         const uint4* p = reinterpret_cast<const uint4*>(src) + my_piece;
         if (src != nullptr) {
-            raw.scales[hf] = __ldg(reinterpret_cast<const uint2*>(src + 384) + hf);
+            raw.scales[hf] = ld_now(reinterpret_cast<const uint2*>(src + 384) + hf);
 #pragma unroll
-            for (int i = hf * (8 / kPieces); i < (hf + 1) * (8 / kPieces); ++i) raw.codes[i] = __ldg(p + kPieces * i);
+            for (int i = hf * (8 / kPieces); i < (hf + 1) * (8 / kPieces); ++i) raw.codes[i] = ld_now(p + kPieces * i);
             if (hf) {
 #pragma unroll
-                for (int i = 0; i < 8 / kPieces; ++i) raw.rope[i] = __ldg(p + 16 + kPieces * i);
+                for (int i = 0; i < 8 / kPieces; ++i) raw.rope[i] = ld_now(p + 16 + kPieces * i);
             }
         }
     };
     const uint8_t *cur = nullptr, *nxt = nullptr;
-    if (producer) {
-        cur = row_of(pg, held);
+    auto first_rows = [&]() {
+        if (id0 >= 0 && id0 < a.n_blocks) cur = a.pool + ((int64_t)id0 * a.be + (e0 - b0 * a.be)) * a.row_bytes;
         load_half(cur, 0);
         load_half(cur, 1);
-    }
-    const Kv4Window wp = kv4_window(a, g, b);
-    const int64_t n = kv4_entries(a, b, status);
-    const int most = sel != nullptr ? a.k : (int)kv4_avail(a, g, n);
-    if (producer) nxt = row_of(pg + kProdGroups, (int)(sel != nullptr ? n : most));
-    // ---- selection length (CSA: the valid prefix of idx): a minimum per warp, joined below
-    if (sel != nullptr) {
+        if (id1 >= 0 && id1 < a.n_blocks) nxt = a.pool + ((int64_t)id1 * a.be + (e1 - b1 * a.be)) * a.row_bytes;
+    };
+    if constexpr (!kCsa) first_rows();
+    const Kv4Window wp = kv4_window(a, x);
+    const int64_t n = kv4_entries(a, x, status);
+    const int most = kCsa ? a.k : (int)kv4_avail(a, x, n);
+    int nsel = most;
+    if (kCsa) {   // its valid prefix: a minimum per warp, joined
         int first_bad = a.k;
-        for (int i = threadIdx.x; i < a.k; i += kTcThreads) {
-            const int32_t v = __ldg(sel + i);
-            if (v < 0 || v >= n) first_bad = min(first_bad, i);
-        }
+        auto look = [&](int i, int32_t v) {
+            if (i < a.k && (v < 0 || v >= n)) first_bad = min(first_bad, i);
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) look((int)threadIdx.x + i * kTcThreads, seen[i]);
+        for (int i = threadIdx.x + 2 * kTcThreads; i < a.k; i += kTcThreads) look(i, __ldg(sel + i));
         first_bad = __reduce_min_sync(0xffffffffu, first_bad);
         if (lane == 0) bars.first_bad[warp] = first_bad;
     }
-    int nsel = most;
-    if (sel != nullptr) {
+    if (kCsa) {
+        first_rows();   // (their table entries come after the selection, which everyone waits for)
         __syncthreads();
         for (int i = 0; i < kTcWarps; ++i) nsel = min(nsel, bars.first_bad[i]);
         // an index past the entries ended it; -1 is the padding
@@ -815,20 +883,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             cp_async_16(dst + (k >> 1) * kBlk + (k & 1 ? wo1 : wo0), src + 16 * kPieces * k, valid);
         cp_async_commit();
     };
-    if (producer && pg >= ncc && pg < nch) copy_window(pg, pg);
+    if (producer && pg == 0 && ncc == 0 && nch > 0) copy_window(0, 0);   // (Q lies in the other stages)
     if (q_warp) {
         const uint32_t neg = a.scale < 0.f ? 0x80008000u : 0u;
         auto q_sync = []() { asm volatile("bar.sync 1, %0;" ::"n"(kQWarps * 32) : "memory"); };
-        cp_async_wait<0>();
-        q_sync();
-        // ---- Q scaled by 2^e (and by the sign of the scale) in place, a warp per head; content to fp16
-#pragma unroll 2
+        warp_wait(&bars.qraw, 0, status, 615);
+        // ---- Q scaled by 2^e (and by the sign of the scale), a warp per head; content to fp16
+#pragma unroll 1
         for (int h = q_id; h < kH; h += kQWarps) {
             const uint32_t at = sw128_off(h, lane & 7);   // chunks lane, lane + 32, lane + 64
             uint4* x0 = reinterpret_cast<uint4*>(q_block(lane >> 3) + at);
             uint4* x1 = reinterpret_cast<uint4*>(q_block(4 + (lane >> 3)) + at);
             uint4* x2 = reinterpret_cast<uint4*>(q_block(8) + at);
-            const uint4 v0 = *x0, v1 = *x1, v2 = *x2;     // (four lanes read each of the last 8 chunks)
+            const uint4 none = make_uint4(0, 0, 0, 0);    // (four lanes read each of the last 8 chunks)
+            const uint4 v0 = h < nh ? q_raw[h * 72 + lane] : none, v1 = h < nh ? q_raw[h * 72 + 32 + lane] : none,
+                        v2 = h < nh ? q_raw[h * 72 + 64 + (lane & 7)] : none;
             uint32_t m2 = bf16x2_maxabs(bf16x2_maxabs(v0.x, v0.y), bf16x2_maxabs(v0.z, v0.w));
             m2 = bf16x2_maxabs(m2, bf16x2_maxabs(bf16x2_maxabs(v1.x, v1.y), bf16x2_maxabs(v1.z, v1.w)));
             m2 = bf16x2_maxabs(m2, bf16x2_maxabs(bf16x2_maxabs(v2.x, v2.y), bf16x2_maxabs(v2.z, v2.w)));
@@ -852,6 +921,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         fence_proxy_async_smem();
         q_sync();
+        // ---- Q's dims 0 .. kTQ-1 into TMEM, both halves of the lanes: three warps per quarter of the lanes, two
+        // column blocks each
+        const int rank = warp < kSoftWarps ? 0 : (warp < kWarpQK - 2 ? 1 : 2), head = (warp & 3) * 16 + (lane & 15);
+        static_assert(kTQ / 64 == 6 && kWarpQK == 16 && kProdWarps == 6, "warps 0-3, 10-13 and 14-17");
+#pragma unroll 1
+        for (int k = 2 * rank; k < 2 * rank + 2; ++k) {
+            uint4 v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(q_block(k) + sw128_off(head, c));
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+                const uint32_t o[8] = {v[c].x, v[c].y, v[c].z, v[c].w, v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
+                tmem_st8(tmem_addr(tmem, (warp & 3) * 32, kTmQ + 32 * k + 4 * c), o);
+            }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.qfull);
     }
     auto chunk_valid = [&](int c) -> int {   // rows of local chunk c
         const int gc = gcof(c);
@@ -928,14 +1016,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t ph = 1;   // of the stage's last release
         for (int c = pg; c < nch; c += kProdGroups) {
             uint8_t* dst = stage_s + st * kStageBytes;
-            // Q's TMEM part leaves the last stage before its first rows come in
+            // Q's TMEM part leaves the last stage (and P) before the first rows come in
             if (c == kStages - 1 && !warp_wait(&bars.qfull, 0, status, 613)) break;
             if (c >= ncc) {
                 // window chunk: bf16 rows by 16-byte cp.async, zeros past the last row; content to fp16 in place
                 if (c >= kStages && (!warp_wait(&bars.kempty[st][0], ph, status, 609) ||
                                      !warp_wait(&bars.kempty[st][1], ph, status, 610)))
                     break;
-                if (c != pg) copy_window(c, st);   // the first is on its way
+                if (c != 0) copy_window(c, st);   // the first is on its way
                 cp_async_wait<0>();
                 uint32_t m2 = 0;
 #pragma unroll 4
@@ -993,7 +1081,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 if (!ok) break;
                 cur = nxt;   // and where the rows of the one after lie
-                if (c + 2 * kProdGroups < ncc) nxt = row_of(c + 2 * kProdGroups, (int)(sel != nullptr ? n : most));
+                if (c + 2 * kProdGroups < ncc) nxt = row_of(c + 2 * kProdGroups, (int)(kCsa ? n : most));
             }
             if ((st += kProdGroups) >= kStages) st -= kStages, ph ^= 1;
         }
@@ -1003,24 +1091,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int head = warp * 16 + (lane & 15), hi16 = lane >> 4;
         float m_used = -INFINITY, l_sum = 0.f;   // log2 domain; weights are 2^(s - m_used + kLift)
         const float sl2 = fabsf(a.scale) * kLog2e * bars.qscale[head];
-        if (nch > 0) {
-            // Q's dims 0 .. kTQ-1 into TMEM, both halves of the lanes
-#pragma unroll 2
-            for (int k = 0; k < kTQ / 64; ++k) {
-                uint4 v[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(q_block(k) + sw128_off(head, c));
-#pragma unroll
-                for (int c = 0; c < 8; c += 2) {
-                    const uint32_t o[8] = {v[c].x, v[c].y, v[c].z, v[c].w, v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
-                    tmem_st8(tmem_addr(tmem, warp * 32, kTmQ + 32 * k + 4 * c), o);
-                }
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.qfull);
-        }
         for (int c = 0; c < nch; ++c) {
             const int pb = c & 1;
             if (!warp_wait(&bars.sfull[pb], (uint32_t)((c >> 1) & 1), status, 620)) break;
@@ -1116,10 +1186,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    // ---- O, eight warps: lane l of warp w holds the O row of head 16 (w & 3) + (l & 15), dims 0-127 (+ 128
-    // for w >= 4, + 256 for l >= 16).  The only split: normalised, staged through shared memory.  One of
+    // ---- O, 16 warps: lane l of warp w holds the O row of head 16 (w & 3) + (l & 15), dims 64 (w / 4) .. + 63
+    // (+ 256 for l >= 16).  The only split: normalised, staged through shared memory.  One of
     // several: the partial as the lanes hold it ([quarter][4 dims][lane], 512 bytes a store).
-    if (warp < 8) {
+    if (warp < 16) {
         tc_fence_after();
         const int quarter = warp & 3, head = quarter * 16 + (lane & 15);
         const float fs = only ? bars.inv_l[head] : 1.f;
@@ -1127,8 +1197,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool f32 = a.out_dtype == LCS_F32;
         uint8_t* rowp = stage_s + head * (f32 ? kOPitchF32 : kOPitchBF16);
         float4* gpart = reinterpret_cast<float4*>(part_o) + ((int64_t)(unit * splits + sp) * 4 + quarter) * (64 * 32) + lane;
-#pragma unroll 1
-        for (int j0 = (warp >> 2) * 8; j0 < (warp >> 2) * 8 + 8; j0 += 4) {
+        {
+            const int j0 = (warp >> 2) * 4;
             uint32_t ov[4][16];
             if (nch > 0) {
 #pragma unroll
@@ -1177,7 +1247,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             *reinterpret_cast<uint4*>(gout + off) = *reinterpret_cast<const uint4*>(stage_s + h * pitch + cb);
         }
     }
-    if (clustered) {
+    if constexpr (kJoin) {
         // a unit's splits are one cluster: its barrier orders the partials, each CTA merges every splits-th task
         cluster_sync_all();
         const int t0 = sp + splits * warp, dt = splits * kTcWarps;
@@ -1218,9 +1288,9 @@ bool use_tc(const AttendKv4Args& a) { return a.q_dtype == LCS_BF16 && a.d_c == k
 
 // Splits per (query, head tile): every CTA resident at once (one per SM); the count that minimises the
 // longest split's chunks plus the merge, both in chunk times (about 1.1 us).  Measured, us a call by
-// splits: 4 chunks of one query 14.1 (1), 16.1 (2); 14 chunks of 32 queries 25.9 (2), 23.4 (3), 20.4
-// (4); 25 of 4: 20.6 (8), 17.7 (9), 16.4 (13); 177 of one 26.7 (16), 22.1 (29), 20.8 (58); 177 of
-// 16: 40.2 (8, clusters), 39.4 (9, merged by a kernel).
+// splits when the rule was made: 4 chunks of one query 14.1 (1), 16.1 (2); 14 chunks of 32 queries 25.9
+// (2), 23.4 (3), 20.4 (4); 25 of 4: 20.6 (8), 17.7 (9), 16.4 (13); 177 of one 26.7 (16), 22.1 (29),
+// 20.8 (58); 177 of 16: 40.2 (8, clusters), 39.4 (9, merged by a kernel).
 int64_t kv4_units(const AttendKv4Args& a) { return a.B * a.Q * ((a.H + kH - 1) / kH); }
 int64_t kv4_entry_chunks(const AttendKv4Args& a) {
     return ((a.idx != nullptr ? a.k : a.max_blocks * a.be) + kChunk - 1) / kChunk;
@@ -1247,20 +1317,28 @@ int64_t kv4_partial_bytes(int64_t units, int64_t splits) {
     return splits == 1 ? 0 : align256(units * splits * kH * kDv * 4) + align256(units * splits * kH * 2 * 4);
 }
 
-// Whether the launch's clusters of `splits` CTAs can all be resident at once (asked once per device and
-// split count; clusters of more than 8 are not portable, but open on this device).
-bool kv4_cluster_ok(int splits, int64_t units) {
+using TcKernel = void (*)(const AttendKv4Args, int, int, float*, float*, int*);
+TcKernel tc_kernel(bool csa, bool join) {
+    return csa ? (join ? attend_kv4_tc_kernel<true, true> : attend_kv4_tc_kernel<true, false>)
+               : (join ? attend_kv4_tc_kernel<false, true> : attend_kv4_tc_kernel<false, false>);
+}
+
+// Whether the launch's clusters of `splits` CTAs can all be resident at once (asked once per kernel, device
+// and split count; clusters of more than 8 are not portable, but open on this device).
+bool kv4_cluster_ok(bool csa, int splits, int64_t units) {
     if (splits < 2 || splits > kMaxCluster) return false;
     constexpr int kDevices = 16;
     static std::mutex mu;
-    static int cache[kDevices][kMaxCluster + 1];
+    static int cache[2][kDevices][kMaxCluster + 1];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return false;
     std::lock_guard<std::mutex> lock(mu);
-    if (cache[dev][splits] == 0) {
+    int& most = cache[csa][dev][splits];
+    if (most == 0) {
+        const TcKernel kern = tc_kernel(csa, true);
         int n = 0;
-        if (set_smem_here(reinterpret_cast<const void*>(attend_kv4_tc_kernel), kTcSmem) == cudaSuccess &&
-            cudaFuncSetAttribute(attend_kv4_tc_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+        if (set_smem_here(reinterpret_cast<const void*>(kern), kTcSmem) == cudaSuccess &&
+            cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)splits);
             cfg.blockDim = dim3(kTcThreads);
@@ -1272,27 +1350,28 @@ bool kv4_cluster_ok(int splits, int64_t units) {
             attr[0].val.clusterDim.z = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&n, attend_kv4_tc_kernel, &cfg) != cudaSuccess) n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
         }
         cudaGetLastError();
-        cache[dev][splits] = n > 0 ? n : -1;
+        most = n > 0 ? n : -1;
     }
-    return cache[dev][splits] >= units;
+    return most >= units;
 }
 
 cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaStream_t s) {
     const int tiles = (a.H + kH - 1) / kH;
     const int64_t units = kv4_units(a);
-    cudaError_t e = set_smem_here(reinterpret_cast<const void*>(attend_kv4_tc_kernel), kTcSmem);
-    if (e != cudaSuccess) return e;
     const int splits = kv4_splits(a);
+    const bool clustered = kv4_cluster_ok(a.idx != nullptr, splits, units);
+    const TcKernel kern = tc_kernel(a.idx != nullptr, clustered);
+    cudaError_t e = set_smem_here(reinterpret_cast<const void*>(kern), kTcSmem);
+    if (e != cudaSuccess) return e;
     float* part_o = nullptr;
     float* part_ml = nullptr;
     if (splits > 1) {
         part_o = static_cast<float*>(scratch);
         part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + align256(units * splits * kH * kDv * 4));
     }
-    const int clustered = kv4_cluster_ok(splits, units) ? 1 : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = splits > 1 ? dim3((unsigned)splits, (unsigned)units) : dim3((unsigned)units);
     cfg.blockDim = dim3(kTcThreads);
@@ -1306,8 +1385,8 @@ cudaError_t launch_tc(const AttendKv4Args& a, void* scratch, int* status, cudaSt
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1 + clustered;
-    e = cudaLaunchKernelEx(&cfg, attend_kv4_tc_kernel, a, tiles, splits, clustered, part_o, part_ml, status);
+    cfg.numAttrs = clustered ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kern, a, tiles, splits, part_o, part_ml, status);
     if (e != cudaSuccess || splits == 1 || clustered) return e;
     // (44 splits of one query: 16 in flight 21.3 us a call, 8 22.8; 9 splits of 16: 40.7 and 39.4)
     return launch_k(splits > 16 ? kv4_merge_kernel<16> : kv4_merge_kernel<8>, dim3((unsigned)(units * 32)), dim3(kMergeThreads), 0, s, true, a, tiles, splits,
