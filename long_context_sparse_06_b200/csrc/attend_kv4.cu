@@ -450,18 +450,18 @@ cudaError_t launch_simt(const AttendKv4Args& a, int* status, cudaStream_t s) {
 //  * Warps 16 and 17 issue the MMAs with the whole warp in step and an elected lane's predicate on
 //    the instruction: 35 cycles per M = 64, N = 64 MMA alone on the SM (32 is its rate), where
 //    issue from a branch of one thread took 55 to 72.
-//  * Q's tile of rows comes in as one bulk copy; every warp but the first group of producers, which
-//    fills the first chunk meanwhile, converts it and moves its TMEM part (12 warps: three per quarter of
-//    TMEM's lanes).
+//  * Every warp but the first group of producers, which fills the first chunk meanwhile, brings in Q,
+//    converts it and moves its TMEM part (12 warps: three per quarter of TMEM's lanes).  (Q in one bulk
+//    copy: a decode step of 16 x 8320 rows 1.0 us faster with its inputs in L2, 1.9 slower from HBM.)
 //  * Warps 0-3 run the online softmax (fp32, exp2).  Weights are kept 2^6 above 1, so that fp16
 //    reaches down to 2^-31 of the largest; O is rescaled when a head's maximum grows by more than 2^8.
 //
-// What a CTA takes, in cycles (hca, 1000 causal queries of 64 heads, 24 chunks each; 267 us in all): 860
-// until TMEM is there, 3000 until Q and the row counts are, 4700 for Q's conversion beside the first
-// chunk's widening, 1100 into TMEM, 2000 to the first S, 2150 a chunk (its MMAs alone: 1680 at M = 64,
+// What a CTA takes, in cycles (hca, 1000 causal queries of 64 heads, 24 chunks each; 270 us in all): 860
+// until TMEM is there, 3800 until Q and the row counts are, 5000 for Q's conversion beside the first
+// chunk's widening, 1100 into TMEM, 1700 to the first S, 2150 a chunk (its MMAs alone: 1680 at M = 64,
 // half the rate of M = 128, which O's 512 columns leave no TMEM for), 4900 for the rest.  csa, 1500 causal
-// queries over 1024 selected rows: 2400 a chunk, its rows scattered; 467 us.  Decode steps: 16 x 8320
-// rows 37.6 us, 32 x 640 19.4, one x 8320 19.5, 4 x 1152 15.6, one of 160 rows 13.0.
+// queries over 1024 selected rows: 2400 a chunk, its rows scattered; 462 us.  Decode steps back to
+// back: 16 x 8320 rows 37.6 us, 32 x 640 19.4, one x 8320 20.8, 4 x 1152 15.9, one of 160 rows 13.6.
 constexpr int kH = 64, kD = 576, kDv = 512, kChunk = 48, kStages = 3;
 constexpr int kBlk = kChunk * 128;            // one SW128 column block of a chunk: 48 rows x 128 B
 constexpr int kStageBytes = 9 * kBlk;         // 54 KB
@@ -482,9 +482,7 @@ constexpr int kMaxSplits = 64, kMaxCluster = 16;
 constexpr int kOPitchF32 = kDv * 4 + 16;      // staged O rows (padded)
 constexpr int kOPitchBF16 = kDv * 2 + 16;
 static_assert(kH * kOPitchF32 <= kStages * kStageBytes, "staged O fits in the stages");
-// Q comes in as it is over stages 1 and 2; what goes to TMEM passes through the end of the stages and P.
-constexpr int kQRawBytes = kH * kD * 2, kQPassAt = kStages * kStageBytes + 2 * kPBytes - kTQ / 64 * kQBlk;
-static_assert(kStageBytes + kQRawBytes <= kQPassAt && kQPassAt >= 2 * kStageBytes && kQPassAt % 1024 == 0, "and stage 0 is free");
+static_assert(kTQ / 64 * kQBlk <= kStageBytes && kH * 128 == kQBlk, "Q's TMEM part passes through the last stage");
 // TMEM columns: O, S (even chunks in lanes 0-15 of each 32, odd ones in lanes 16-31), Q (twice, for
 // both halves of the lanes).
 constexpr uint32_t kTmS = 256, kTmQ = kTmS + kChunk, kHi16 = 16u << 16;
@@ -499,7 +497,7 @@ struct TcBars {
     uint64_t pfull[2];
     uint64_t ofull[2];                        // P.V of the chunk done
     uint64_t odone;                           // every P.V of this CTA done
-    uint64_t qraw, qfull;                     // Q has come in; Q is where the MMAs read it
+    uint64_t qfull;                           // Q is where the MMAs read it
     uint32_t tmem_base;
     int first_bad[kTcWarps];
     float qscale[kH];                         // 2^-e of head h: the true q is the stored one times it
@@ -766,7 +764,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&bars.ofull[i], 1);
         }
         mbar_init(&bars.odone, 1);
-        mbar_init(&bars.qraw, 1);
         mbar_init(&bars.qfull, kQWarps);
         fence_barrier_init();
     }
@@ -781,23 +778,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #if defined(__CUDA_ARCH__)
     asm volatile("griddepcontrol.wait;" ::: "memory");   // everything above reads no memory of the call
 #endif
-    // column block k of Q, 16-byte pieces of it as it came in
-    auto q_block = [&](int k) { return k < kTQ / 64 ? stage_s + kQPassAt + k * kQBlk : q_s + (k - kTQ / 64) * kQBlk; };
-    const uint4* q_raw = reinterpret_cast<const uint4*>(stage_s + kStageBytes);
-    // Q is converted by every warp but the first group of producers, which fills the first chunk meanwhile
-    const bool q_warp = !producer || pg != 0;
-    const int q_id = warp < kSoftWarps ? warp : warp - kProdWarps;   // 0 .. kQWarps - 1
-    // ---- the loads that nothing waits for, before everything else: Q, a tile of rows in one piece ...
-    if (threadIdx.x == 0) {
-        mbar_arrive_expect_tx(&bars.qraw, (uint32_t)(nh * kD * 2));
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(q_raw)),
-                     "l"(static_cast<const uint8_t*>(a.q) + ((int64_t)g * a.H + h0) * (kD * 2)), "r"(nh * kD * 2), "r"(smem_u32(&bars.qraw))
-                     : "memory");
-    }
-    const Kv4Query x = kv4_query(a, g, b);
-    // ... the selection (CSA), of which the valid prefix counts, and the producers' first two rows: a group takes
-    // every other chunk.  How many entries there are, and which of a chunk's rows are attended (the
-    // selection's length), is known later: rows past it are dropped when they are widened.
+    // column block k of Q: the first ones pass through the last stage into TMEM
+    auto q_block = [&](int k) { return k < kTQ / 64 ? stage_s + (kStages - 1) * kStageBytes + k * kQBlk : q_s + (k - kTQ / 64) * kQBlk; };
+    // ---- the loads that nothing waits for, before everything else: the selection (CSA), of which the valid
+    // prefix counts, and the producers' first two rows (a group takes every other chunk).  How many entries
+    // there are, and which of a chunk's rows are attended (the selection's length), is known later: rows
+    // past it are dropped when they are widened ...
     const int32_t* sel = kCsa ? a.idx + (int64_t)g * a.k : nullptr;
     const int held = (int)(a.max_blocks * a.be);   // entries that the table can hold
     auto gcof = [&](int c) -> int { return sp + splits * c; };
@@ -813,10 +799,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < 2; ++i)
             if ((int)threadIdx.x + i * kTcThreads < a.k) seen[i] = ld_now(sel + threadIdx.x + i * kTcThreads);
     }
-    const bool in0 = e0 >= 0 && e0 < held, in1 = e1 >= 0 && e1 < held;
-    const int b0 = in0 ? e0 / a.be : 0, b1 = in1 ? e1 / a.be : 0;
-    const int32_t id0 = in0 ? ld_now(a.table + (int64_t)b * a.max_blocks + b0) : -1;
-    const int32_t id1 = in1 ? ld_now(a.table + (int64_t)b * a.max_blocks + b1) : -1;
+    // ... and Q as it is, in the SW128 layout (by every warp but the first group of producers, which fills the
+    // first chunk meanwhile)
+    const Kv4Query x = kv4_query(a, g, b);
+    const bool q_warp = !producer || pg != 0;
+    const int q_id = warp < kSoftWarps ? warp : warp - kProdWarps;   // 0 .. kQWarps - 1
+    if (q_warp) {
+        const uint8_t* qg = static_cast<const uint8_t*>(a.q) + ((int64_t)g * a.H + h0) * (kD * 2);
+        static_assert(kQWarps * 32 == 384 && kH * 72 % 384 == 0, "twelve pieces a thread, 5 rows and 24 pieces apart");
+        int h = (q_id * 32 + lane) / 72, c = (q_id * 32 + lane) - h * 72;
+#pragma unroll 1
+        for (int i = q_id * 32 + lane; i < kH * 72; i += 384) {
+            cp_async_16(q_block(c >> 3) + sw128_off(h, c & 7), qg + (h < nh ? i * 16 : 0), h < nh);
+            h += 5, c += 24;
+            if (c >= 72) c -= 72, ++h;
+        }
+        cp_async_commit();
+    }
     auto row_of = [&](int c, int lim) -> const uint8_t* {   // this lane's row of local chunk c, null if there is none
         const int j = gcof(c) * kChunk + my_row;
         if (j >= (kCsa ? a.k : lim)) return nullptr;
@@ -836,19 +835,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
     };
-    const uint8_t *cur = nullptr, *nxt = nullptr;
-    auto first_rows = [&]() {
-        if (id0 >= 0 && id0 < a.n_blocks) cur = a.pool + ((int64_t)id0 * a.be + (e0 - b0 * a.be)) * a.row_bytes;
-        load_half(cur, 0);
-        load_half(cur, 1);
-        if (id1 >= 0 && id1 < a.n_blocks) nxt = a.pool + ((int64_t)id1 * a.be + (e1 - b1 * a.be)) * a.row_bytes;
-    };
-    if constexpr (!kCsa) first_rows();
+    const bool in0 = e0 >= 0 && e0 < held, in1 = e1 >= 0 && e1 < held;
+    const int b0 = in0 ? e0 / a.be : 0, b1 = in1 ? e1 / a.be : 0;
+    const int32_t id0 = in0 ? ld_now(a.table + (int64_t)b * a.max_blocks + b0) : -1;
+    const int32_t id1 = in1 ? ld_now(a.table + (int64_t)b * a.max_blocks + b1) : -1;
     const Kv4Window wp = kv4_window(a, x);
     const int64_t n = kv4_entries(a, x, status);
     const int most = kCsa ? a.k : (int)kv4_avail(a, x, n);
     int nsel = most;
-    if (kCsa) {   // its valid prefix: a minimum per warp, joined
+    if (kCsa) {   // the selection's valid prefix: a minimum per warp, joined
         int first_bad = a.k;
         auto look = [&](int i, int32_t v) {
             if (i < a.k && (v < 0 || v >= n)) first_bad = min(first_bad, i);
@@ -859,8 +854,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         first_bad = __reduce_min_sync(0xffffffffu, first_bad);
         if (lane == 0) bars.first_bad[warp] = first_bad;
     }
+    const uint8_t *cur = nullptr, *nxt = nullptr;
+    if (id0 >= 0 && id0 < a.n_blocks) cur = a.pool + ((int64_t)id0 * a.be + (e0 - b0 * a.be)) * a.row_bytes;
+    load_half(cur, 0);
+    load_half(cur, 1);
+    if (id1 >= 0 && id1 < a.n_blocks) nxt = a.pool + ((int64_t)id1 * a.be + (e1 - b1 * a.be)) * a.row_bytes;
     if (kCsa) {
-        first_rows();   // (their table entries come after the selection, which everyone waits for)
         __syncthreads();
         for (int i = 0; i < kTcWarps; ++i) nsel = min(nsel, bars.first_bad[i]);
         // an index past the entries ended it; -1 is the padding
@@ -883,21 +882,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             cp_async_16(dst + (k >> 1) * kBlk + (k & 1 ? wo1 : wo0), src + 16 * kPieces * k, valid);
         cp_async_commit();
     };
-    if (producer && pg == 0 && ncc == 0 && nch > 0) copy_window(0, 0);   // (Q lies in the other stages)
+    if (producer && pg >= ncc && pg < nch) copy_window(pg, pg);
     if (q_warp) {
         const uint32_t neg = a.scale < 0.f ? 0x80008000u : 0u;
         auto q_sync = []() { asm volatile("bar.sync 1, %0;" ::"n"(kQWarps * 32) : "memory"); };
-        warp_wait(&bars.qraw, 0, status, 615);
-        // ---- Q scaled by 2^e (and by the sign of the scale), a warp per head; content to fp16
+        cp_async_wait<0>();
+        q_sync();
+        // ---- Q scaled by 2^e (and by the sign of the scale) in place, a warp per head; content to fp16
 #pragma unroll 1
         for (int h = q_id; h < kH; h += kQWarps) {
             const uint32_t at = sw128_off(h, lane & 7);   // chunks lane, lane + 32, lane + 64
             uint4* x0 = reinterpret_cast<uint4*>(q_block(lane >> 3) + at);
             uint4* x1 = reinterpret_cast<uint4*>(q_block(4 + (lane >> 3)) + at);
             uint4* x2 = reinterpret_cast<uint4*>(q_block(8) + at);
-            const uint4 none = make_uint4(0, 0, 0, 0);    // (four lanes read each of the last 8 chunks)
-            const uint4 v0 = h < nh ? q_raw[h * 72 + lane] : none, v1 = h < nh ? q_raw[h * 72 + 32 + lane] : none,
-                        v2 = h < nh ? q_raw[h * 72 + 64 + (lane & 7)] : none;
+            const uint4 v0 = *x0, v1 = *x1, v2 = *x2;     // (four lanes read each of the last 8 chunks)
             uint32_t m2 = bf16x2_maxabs(bf16x2_maxabs(v0.x, v0.y), bf16x2_maxabs(v0.z, v0.w));
             m2 = bf16x2_maxabs(m2, bf16x2_maxabs(bf16x2_maxabs(v1.x, v1.y), bf16x2_maxabs(v1.z, v1.w)));
             m2 = bf16x2_maxabs(m2, bf16x2_maxabs(bf16x2_maxabs(v2.x, v2.y), bf16x2_maxabs(v2.z, v2.w)));
@@ -1016,14 +1014,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t ph = 1;   // of the stage's last release
         for (int c = pg; c < nch; c += kProdGroups) {
             uint8_t* dst = stage_s + st * kStageBytes;
-            // Q's TMEM part leaves the last stage (and P) before the first rows come in
+            // Q's TMEM part leaves the last stage before its first rows come in
             if (c == kStages - 1 && !warp_wait(&bars.qfull, 0, status, 613)) break;
             if (c >= ncc) {
                 // window chunk: bf16 rows by 16-byte cp.async, zeros past the last row; content to fp16 in place
                 if (c >= kStages && (!warp_wait(&bars.kempty[st][0], ph, status, 609) ||
                                      !warp_wait(&bars.kempty[st][1], ph, status, 610)))
                     break;
-                if (c != 0) copy_window(c, st);   // the first is on its way
+                if (c != pg) copy_window(c, st);   // the first is on its way
                 cp_async_wait<0>();
                 uint32_t m2 = 0;
 #pragma unroll 4
