@@ -598,9 +598,11 @@ static int run_attend_kv4(const AttendKv4Args& a, void* ws, size_t ws_bytes, cud
     if (a.B * a.Q > 0 && (a.q == nullptr || a.out == nullptr || a.n_entries == nullptr)) return LCS_ERR_INVALID;
     if (a.B * a.Q > 0 && a.B * a.max_blocks > 0 && (a.table == nullptr || a.pool == nullptr)) return LCS_ERR_INVALID;
     if (a.B * a.Q > 0 && a.Tw > 0 && a.win == nullptr) return LCS_ERR_INVALID;
-    if ((a.q_pos == nullptr) != (a.win_pos0 == nullptr)) return LCS_ERR_INVALID;
-    if (a.q_pos == nullptr && a.Q != 1) return LCS_ERR_INVALID;
-    if (a.q_pos != nullptr && a.n_win != nullptr) return LCS_ERR_INVALID;
+    if (a.B * a.Q > 0) {   // (empty arrays may have no address)
+        if ((a.q_pos == nullptr) != (a.win_pos0 == nullptr)) return LCS_ERR_INVALID;
+        if (a.q_pos == nullptr && a.Q != 1) return LCS_ERR_INVALID;
+        if (a.q_pos != nullptr && a.n_win != nullptr) return LCS_ERR_INVALID;
+    }
     if (!aligned16(a.q) || !aligned16(a.pool) || !aligned16(a.win) || !aligned16(a.out)) return LCS_ERR_INVALID;
     if (a.max_blocks >= (int64_t(1) << 31) / a.be || a.B >= (int64_t(1) << 24) || a.Q >= (int64_t(1) << 31) ||
         a.B * a.Q * 2 >= (int64_t(1) << 31) || a.Tw >= (int64_t(1) << 31) || a.n_blocks >= (int64_t(1) << 31))

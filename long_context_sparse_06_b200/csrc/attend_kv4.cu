@@ -1293,12 +1293,16 @@ int64_t kv4_units(const AttendKv4Args& a) { return a.B * a.Q * ((a.H + kH - 1) /
 int64_t kv4_entry_chunks(const AttendKv4Args& a) {
     return ((a.idx != nullptr ? a.k : a.max_blocks * a.be) + kChunk - 1) / kChunk;
 }
-int kv4_splits_of(int64_t units, int64_t chunks) {
+int kv4_splits_of(int64_t units, int64_t chunks) {   // (a call's host time: 32-bit whole numbers, 1/32 of a chunk)
+    const int sms = num_sms();
+    if (units < 1 || units * 2 > sms || chunks < 2) return 1;
+    const unsigned n = (unsigned)(chunks < (1 << 26) ? chunks : 1 << 26);
+    const int most = (int)(sms / units < kMaxSplits ? sms / units : kMaxSplits), u = (int)units;
     int best = 1;
-    double best_cost = (double)chunks;
-    for (int s = 2; s <= kMaxSplits && s <= chunks && units * s <= num_sms(); ++s) {
-        const bool cluster = s <= 8 || (s == kMaxCluster && units * s <= num_sms() / 2);
-        const double cost = (double)((chunks + s - 1) / s) + (cluster ? 3.5 : 4.5 + s / 32.0);
+    unsigned best_cost = 32u * n;
+    for (int s = 2; s <= most && (unsigned)s <= n; ++s) {
+        const bool cluster = s <= 8 || (s == kMaxCluster && u * s <= sms / 2);
+        const unsigned cost = 32u * ((n + s - 1) / s) + (cluster ? 112u : 144u + s);   // 3.5, or 4.5 + s / 32, chunk times
         if (cost < best_cost) {
             best = s;
             best_cost = cost;

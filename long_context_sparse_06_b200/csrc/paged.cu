@@ -23,7 +23,9 @@ namespace {
 // Every CTA repeats the scan (a few KB of lengths, from L2) and then writes its share of
 // the outputs, so that the call is one launch: a decode step's plan is bound by the launch,
 // a batch of prompts by the slots it writes.  An entry's block id comes from the free list
-// directly when this call assigns it, so no CTA waits for another's table writes.
+// directly when this call assigns it, so no CTA waits for another's table writes.  32 requests of one
+// token each: 5.0 us a call back to back; 64 prompts with 1.05 million slots: 11.8 (22.7 with four
+// neighbouring slots a thread, each looked up by itself), half of it the scan and the launch.
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxB = 8192;
 

@@ -172,6 +172,7 @@ def test_refusals_without_device(L):
     assert lib.lcs_workspace_size(L.OP_ATTEND_KV4, 2, 1, 128, 128, 8, 64, 512, 0) >= 256
     if not torch.cuda.is_available():
         assert plan() == -3 and csa() == -3 and hca() == -3
+        assert plan(B=0) == -3 and csa(B=0) == -3 and hca(B=0) == -3 and hca(Q=0, qp=P, wp=P) == -3
         assert lib.lcs_kv4_store(P, 0, 4, 512, 64, P, P, 8, P, 256, None) == -3
         assert lib.lcs_kv4_load(P, 8, P, 4, 512, 64, P, 1, P, 256, None) == -3
 
@@ -924,6 +925,32 @@ def test_stream_argument_without_a_workspace(G):
     st.synchronize()
     assert torch.equal(G.lcs_kv4_load(own, slots, out_dtype=torch.float32).double(), decode_rows(own[:40], 512, 64))
     assert tab.tolist() == [[5, 2, 9, -1]] and plan[4].item() == 3
+
+
+@gpu
+def test_nothing_to_do(G):
+    """No requests, no queries, no rows, no blocks: empty results, and no row seen gives zeros."""
+    z = lambda *s, dt=torch.int64: torch.zeros(s, dtype=dt, device=DEV)
+    i32, u8 = torch.int32, torch.uint8
+    pool = make_pool(G, 4, 16, 512, 64, 3)
+    for H, dc, dr, dt in ((64, 512, 64, BF), (3, 64, 8, torch.float32)):
+        p = pool if dc == 512 else make_pool(G, 4, 16, dc, dr, 4)
+        o = G.hca_attend_kv4(z(0, 1, H, dc + dr, dt=dt), p, z(0, 3, dt=i32), z(0), None, 0.1, d_c=dc)
+        assert o.shape == (0, 1, H, dc)
+        o = G.csa_attend_kv4(z(2, 0, H, dc + dr, dt=dt), p, z(2, 3, dt=i32), z(2), None, z(2, 0, 5, dt=i32), 0.1, d_c=dc, q_pos=z(2, 0), win_pos0=z(2))
+        assert o.shape == (2, 0, H, dc)
+        q = torch.ones((2, 1, H, dc + dr), device=DEV).to(dt)
+        for table, win in ((z(2, 0, dt=i32), None), (z(2, 3, dt=i32), torch.ones((2, 4, dc + dr), device=DEV).to(dt))):
+            o, lse = G.hca_attend_kv4(q, p, table, z(2), win, 0.1, d_c=dc, n_win=z(2), want_lse=True)
+            assert (o == 0).all() and (lse == -math.inf).all()
+            o, lse = G.csa_attend_kv4(q, p, table, z(2), win, z(2, 1, 0, dt=i32), 0.1, d_c=dc, n_win=z(2), want_lse=True)
+            assert (o == 0).all() and (lse == -math.inf).all()
+    G.lcs_kv4_store(z(0, 576, dt=BF), z(0), pool)
+    assert G.lcs_kv4_load(pool, z(0)).shape == (0, 576)
+    ws = G.workspace(256)
+    none = z(0, 16, 400, dt=u8)
+    G.lcs_kv4_store(torch.ones((2, 576), device=DEV), torch.tensor([-1, -1], device=DEV), none, ws=ws)
+    assert (G.lcs_kv4_load(none, torch.tensor([-1], device=DEV), ws=ws) == 0).all() and G.lcs_status(ws) == 0
 
 
 @gpu
