@@ -901,6 +901,31 @@ def test_one_workspace_for_calls_in_turn(G):
 
 
 @gpu
+def test_two_graphs_at_once(G):
+    """Two captured decode steps with a workspace each, replayed on two streams at the same time."""
+    pool = make_pool(G, 200, 32, 512, 64, 9)
+    steps = []
+    for i, B in enumerate((4, 9)):
+        q = torch.randn((B, 1, 64, 576), generator=gen(20 + i), device=DEV).to(BF)
+        table = torch.randint(0, 200, (B, 60), generator=gen(30 + i), device=DEV, dtype=torch.int32)
+        n = torch.randint(0, 60 * 32, (B,), generator=gen(40 + i), device=DEV)
+        want = G.hca_attend_kv4(q, pool, table, n, None, 1 / 24)
+        ws = G.workspace(G.lcs_workspace_size(G.OP_ATTEND_KV4, B, 1, 60 * 32, 0, 0))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = [G.hca_attend_kv4(q, pool, table, n, None, 1 / 24, ws=ws) for _ in range(20)]
+        steps.append((graph, outs, want, torch.cuda.Stream(), ws, (q, table, n)))   # (a graph keeps no inputs alive)
+    for _ in range(3):
+        for graph, _, _, st, _, _ in steps:
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, outs, want, _, ws, _ in steps:
+        assert all(torch.equal(o, want) for o in outs) and G.lcs_status(ws) == 0
+
+
+@gpu
 def test_stream_argument_without_a_workspace(G):
     """What the call allocates belongs to the given stream: work on the current one does not touch it."""
     pool = make_pool(G, 64, 32, 512, 64, 8)
@@ -990,16 +1015,22 @@ slots = torch.arange(2048, device='cuda')
 table = torch.arange(64, dtype=torch.int32, device='cuda').view(1, 64)
 n = torch.tensor([2000], device='cuda')
 q = torch.randn((1, 1, 64, 576), generator=g, device='cuda').bfloat16()
-ws = L.workspace(L.lcs_workspace_size(L.OP_ATTEND_KV4, 1, 1, 2048, 0, 0))
+short, m = table[:, :10].contiguous(), torch.tensor([300], device='cuda')
+idx = torch.arange(0, 1500, 5, dtype=torch.int32, device='cuda').view(1, 1, 300)
+ws = L.workspace(max(L.lcs_workspace_size(L.OP_ATTEND_KV4, 1, 1, N, 0, k) for N, k in ((2048, 0), (320, 0), (2048, 300))))
 torch.cuda.synchronize()
 graph = torch.cuda.CUDAGraph()
 with torch.cuda.graph(graph):
     L.lcs_kv4_store(x, slots, pool, ws=ws)
     o = L.hca_attend_kv4(q, pool, table, n, None, 1 / 24, ws=ws)
     p = L.hca_attend_kv4(q.float(), pool, table, n, None, 1 / 24, ws=ws)
+    few = L.hca_attend_kv4(q, pool, short, m, None, 1 / 24, ws=ws)      # seven splits, one cluster
+    sel = L.csa_attend_kv4(q, pool, table, n, None, idx, 1 / 24, ws=ws)
 graph.replay()
 torch.cuda.synchronize()
 assert torch.equal(o, L.hca_attend_kv4(q, pool, table, n, None, 1 / 24))
+assert torch.equal(few, L.hca_attend_kv4(q, pool, short, m, None, 1 / 24))
+assert torch.equal(sel, L.csa_attend_kv4(q, pool, table, n, None, idx, 1 / 24))
 assert (o.float() - p).abs().max() < 0.05 and p.abs().max() > 0.01
 assert L.lcs_status(ws) == 0
 print('captured')
