@@ -396,9 +396,10 @@ LCS_API int lcs_kv4_load(const void* pool, int64_t n_slots, const int64_t* slots
  * content is exact from 2^-14 up, off by at most 2^-25 below, and a magnitude of 2^16 or more
  * records LCS_ERR_DEVICE; a weight is off by at most 2^-11 of itself.  RoPE dims stay bf16: of
  * magnitude below 2^100, so that fp32 sums hold (on either path |scale q.K| <= 2^23 and
- * finite q and attended rows; other outputs are unspecified).  q,
- * pool, win and out on 16 bytes; max_blocks * block_entries + Tw < 2^31 - 2^16.  Workspace: lcs_workspace_size(LCS_OP_ATTEND_KV4, B, Q, N_c =
- * max_blocks * block_entries, Tw, k (0 for HCA), H, d_v = d_c, 0).
+ * finite q and attended rows; other outputs are unspecified).  q, pool, win and out on 16
+ * bytes; max_blocks * block_entries + Tw < 2^31 - 2^16.  Workspace: lcs_workspace_size(
+ * LCS_OP_ATTEND_KV4, B, Q, N_c = max_blocks * block_entries, Tw, k (0 for HCA), H, d_v = d_c, 0),
+ * for every W.
  */
 LCS_API int csa_attend_kv4(const void* q, int q_dtype, const void* pool, int64_t n_blocks, int block_entries,
                  const int32_t* block_table, int64_t max_blocks, const int64_t* n_entries, const void* win,

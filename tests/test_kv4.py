@@ -10,9 +10,10 @@ Tolerances (derived, per element, from the data of the test):
     path sums D terms with a rounding of 2^-24 each: D * 2^-24 in place of (D/16 + 2) * 2^-23);
   * a weight p_r / l then has the relative error 2 delta (its own and the sum's) + 2^-21 (exp2 and
     the scaling of its argument: arguments up to 2^5 lose 2^-24 * 2^5 = 2^-19: counted as 2^-18),
-    plus its own rounding, 2^-11 (fp16; none on the CUDA cores); window content below 2^-14 is
-    off by 2^-25 on the tensor cores (fp16's subnormals); weights below the smallest fp16 step 2^-24 / 2^6 of the largest lose that much
-    absolutely; the sum over R rows in fp32 adds (R/16 + 2) * 2^-23 of sum p|v|;
+    plus its own rounding, 2^-11 (fp16; none on the CUDA cores); window content below 2^-14 is off by
+    2^-25 on the tensor cores (fp16's subnormals), in the scores and in the values; weights below the
+    smallest fp16 step 2^-24 / 2^6 of the largest lose that much absolutely; the sum over R rows in fp32
+    adds (R/16 + 2) * 2^-23 of sum p|v|;
   * a bf16 output is off by half a step, 2^-8 |o|; fp32 by 2^-24 |o|.
 """
 import math
