@@ -456,11 +456,11 @@ cudaError_t launch_simt(const AttendKv4Args& a, int* status, cudaStream_t s) {
 //  * Warps 0-3 run the online softmax (fp32, exp2).  Weights are kept 2^6 above 1, so that fp16
 //    reaches down to 2^-31 of the largest; O is rescaled when a head's maximum grows by more than 2^8.
 //
-// What a CTA takes, in cycles (hca, 1000 causal queries of 64 heads, 24 chunks each; 270 us in all): 860
+// What a CTA takes, in cycles (hca, 1000 causal queries of 64 heads, 24 chunks each; 269 us in all): 860
 // until TMEM is there, 3800 until Q and the row counts are, 5000 for Q's conversion beside the first
 // chunk's widening, 1100 into TMEM, 1700 to the first S, 2150 a chunk (its MMAs alone: 1680 at M = 64,
 // half the rate of M = 128, which O's 512 columns leave no TMEM for), 4900 for the rest.  csa, 1500 causal
-// queries over 1024 selected rows: 2400 a chunk, its rows scattered; 462 us.  Decode steps back to
+// queries over 1024 selected rows: 2400 a chunk, its rows scattered; 457 us.  Decode steps back to
 // back: 16 x 8320 rows 37.6 us, 32 x 640 19.4, one x 8320 20.8, 4 x 1152 15.9, one of 160 rows 13.6.
 constexpr int kH = 64, kD = 576, kDv = 512, kChunk = 48, kStages = 3;
 constexpr int kBlk = kChunk * 128;            // one SW128 column block of a chunk: 48 rows x 128 B
@@ -870,14 +870,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int nch = uni(sp < nch_all ? (nch_all - sp + splits - 1) / splits : 0);
     const int ncc = uni(sp < ncc_all ? (ncc_all - sp + splits - 1) / splits : 0);
     // window chunk c into its stage: bf16 rows by 16-byte cp.async, pieces my_piece + 4 k of this lane's row, zeros
-    // past the last row
+    // past the last row (all 18 copies unrolled: csa prefill 461 us, 457 with two, whose code is shorter)
     const uint32_t wo0 = sw128_off(my_row, my_piece), wo1 = sw128_off(my_row, my_piece + kPieces);
     auto copy_window = [&](int c, int st) {
         uint8_t* dst = stage_s + st * kStageBytes;
         const int r = (gcof(c) - ncc_all) * kChunk + my_row;
         const bool valid = r < (int)wp.n;
         const uint8_t* src = static_cast<const uint8_t*>(a.win) + (((int64_t)b * a.Tw + wp.lo + (valid ? r : 0)) * kD) * 2 + 16 * my_piece;
-#pragma unroll
+#pragma unroll 2
         for (int k = 0; k < 72 / kPieces; ++k)
             cp_async_16(dst + (k >> 1) * kBlk + (k & 1 ? wo1 : wo0), src + 16 * kPieces * k, valid);
         cp_async_commit();
