@@ -515,6 +515,17 @@ LCS_API int lcs_clear_status(void* ws, cudaStream_t stream);
  */
 LCS_API int lcs_selftest_wait(int budget_us, void* ws, size_t ws_bytes, long long* out, cudaStream_t stream);
 
+/*
+ * Self-test of the waits of csa_attend_kv4 and hca_attend_kv4: one warp waits on an mbarrier
+ * that another completes after delay_us microseconds (1..1e6), under the status word that ws
+ * holds (it is not cleared).  An error of the data (LCS_ERR_DEVICE, recorded for another
+ * request) does not end the wait; LCS_ERR_TIMEOUT, or a wait that ran out after an error was
+ * recorded, does.
+ *   out  2 device int64: [the wait succeeded (0/1), its ns]
+ * Returns as lcs_selftest_wait.
+ */
+LCS_API int lcs_selftest_warp_wait(int delay_us, void* ws, size_t ws_bytes, long long* out, cudaStream_t stream);
+
 /* Static description of a status code. */
 LCS_API const char* lcs_error_string(int code);
 

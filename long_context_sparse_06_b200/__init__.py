@@ -16,7 +16,7 @@ __all__ = [
     "F32", "BF16", "KV_FP8", "FP4", "KV_FP4", "MODE_CSA", "MODE_HCA", "LcsError", "lib",
     "csa_compress", "hca_compress", "lcs_compress_proj", "csa_index_topk", "csa_index_topk_proj", "lcs_topk", "csa_attend", "hca_attend",
     "decode_fused", "lcs_cache_append", "lcs_cp_candidates", "lcs_cp_select", "lcs_attn_merge", "lcs_page_plan", "lcs_kv4_store", "lcs_kv4_load", "csa_attend_kv4", "hca_attend_kv4", "kv_fp4_row_bytes", "group_oproj", "lcs_rope", "lcs_quant_kv_fp8", "lcs_quant_fp4",
-    "lcs_workspace_size", "lcs_status", "lcs_clear_status", "lcs_selftest_wait", "workspace", "kv_fp8_row_bytes",
+    "lcs_workspace_size", "lcs_status", "lcs_clear_status", "lcs_selftest_wait", "lcs_selftest_warp_wait", "workspace", "kv_fp8_row_bytes",
 ]
 
 F32, BF16, KV_FP8, FP4, KV_FP4 = 0, 1, 2, 3, 4
@@ -76,6 +76,7 @@ def lib():
             "lcs_status": [P, P],
             "lcs_clear_status": [P, P],
             "lcs_selftest_wait": [I, P, SZ, P, P],
+            "lcs_selftest_warp_wait": [I, P, SZ, P, P],
             "lcs_set_stage_events": [P, I],
         }
         for name, args in sig.items():
@@ -154,6 +155,11 @@ def lcs_clear_status(ws, stream=None):
 def lcs_selftest_wait(budget_us, ws, out, stream=None):
     """Runs the bounded-wait self-test; out is a 4-element int64 device tensor."""
     _call("lcs_selftest_wait", int(budget_us), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), _stream(stream))
+
+
+def lcs_selftest_warp_wait(delay_us, ws, out, stream=None):
+    """Runs the self-test of the 4-bit attention's waits; out is a 2-element int64 device tensor."""
+    _call("lcs_selftest_warp_wait", int(delay_us), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), _stream(stream))
 
 
 # ---------------------------------------------------------------- compressor

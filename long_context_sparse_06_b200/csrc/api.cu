@@ -240,6 +240,13 @@ int lcs_selftest_wait(int budget_us, void* ws, size_t ws_bytes, long long* out, 
     return from_cuda(launch_selftest_wait((uint64_t)budget_us * 1000ull, static_cast<int*>(ws), out, stream));
 }
 
+int lcs_selftest_warp_wait(int delay_us, void* ws, size_t ws_bytes, long long* out, cudaStream_t stream) {
+    if (ws == nullptr || out == nullptr || ws_bytes < (size_t)kStatusBytes) return LCS_ERR_INVALID;
+    if (delay_us < 1 || delay_us > 1000000) return LCS_ERR_INVALID;
+    if (!device_ok()) return LCS_ERR_CUDA;
+    return from_cuda(launch_selftest_warp_wait((uint64_t)delay_us * 1000ull, static_cast<int*>(ws), out, stream));
+}
+
 int lcs_status(void* ws, cudaStream_t stream) {
     if (ws == nullptr) return LCS_ERR_INVALID;
     if (!device_ok()) return LCS_ERR_CUDA;

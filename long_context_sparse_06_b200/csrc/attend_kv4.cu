@@ -549,8 +549,9 @@ __device__ __forceinline__ void commit_if(uint32_t on, uint64_t* bar) {
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t bf16) { return bf16 & ~((1u << 7) | (1u << 10)); }
 
 // A bounded wait that the whole warp leaves with one answer.  The thread sleeps in the hardware's wait
-// (up to the hint, 20 us) instead of polling.  The clock and the grid's status word are looked at
-// after every 16 sleeps.
+// (up to the hint, 20 us) instead of polling.  The clock and the workspace's status words are looked at
+// after every 16 sleeps: another wait that ran out (whether it or an earlier error is the one recorded) ends
+// this one, an error in a request's data does not, since only that request's output may suffer from it.
 __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -570,8 +571,12 @@ __device__ __noinline__ bool warp_wait_on(uint64_t* bar, uint32_t parity, int* s
         const uint64_t now = globaltimer();
         if (t0 == 0) t0 = now;
         const bool late = now - t0 > kWaitBudgetNs;
-        if (late) set_status(status, LCS_ERR_TIMEOUT, where);
-        if (__any_sync(0xffffffffu, late || *(volatile int*)status != 0)) return false;
+        volatile int* st = status;
+        if (late) {
+            set_status(status, LCS_ERR_TIMEOUT, where);
+            st[2] = LCS_ERR_TIMEOUT;
+        }
+        if (__any_sync(0xffffffffu, late || st[0] == LCS_ERR_TIMEOUT || st[2] == LCS_ERR_TIMEOUT)) return false;
     }
 }
 
@@ -1282,6 +1287,30 @@ __global__ void __launch_bounds__(kMergeThreads)
 #endif
 }
 
+// The waits above on a barrier that warp 1 completes after delay_ns: out = {warp 0 saw it complete, its ns}.
+__global__ void selftest_warp_wait_kernel(uint64_t delay_ns, int* status, long long* out) {
+    __shared__ uint64_t bar;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const uint64_t t0 = globaltimer();
+    if (threadIdx.x < 32) {
+        const bool ok = warp_wait(&bar, 0, status, 903);
+        const uint64_t t1 = globaltimer();
+        if (threadIdx.x == 0) {
+            out[0] = ok;
+            out[1] = (long long)(t1 - t0);
+        }
+    } else {
+        for (int i = 0; i < (1 << 20) && globaltimer() - t0 < delay_ns; ++i) __nanosleep(1000);
+        __syncwarp();
+        if (threadIdx.x == 32) mbar_arrive(&bar);
+    }
+    __syncthreads();
+}
+
 bool use_tc(const AttendKv4Args& a) { return a.q_dtype == LCS_BF16 && a.d_c == kDv && a.d_r == kD - kDv; }
 
 // Splits per (query, head tile): every CTA resident at once (one per SM); the count that minimises the
@@ -1418,6 +1447,11 @@ int64_t attend_kv4_scratch_bound(const AttendKv4Args& a) {
         if (s > entries + window) s = entries + window;
     }
     return kv4_partial_bytes(units, s);
+}
+
+cudaError_t launch_selftest_warp_wait(uint64_t delay_ns, int* status, long long* out, cudaStream_t stream) {
+    selftest_warp_wait_kernel<<<1, 64, 0, stream>>>(delay_ns, status, out);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_attend_kv4(const AttendKv4Args& a, void* scratch, int* status, cudaStream_t s) {

@@ -24,7 +24,8 @@ namespace lcs {
 // ---------------------------------------------------------------- status word
 // The first 256 bytes of every workspace.  status[0] holds the first error code
 // recorded by any kernel since it was last cleared; status[1] a detail word
-// (which wait gave up).
+// (which wait gave up); status[2] is LCS_ERR_TIMEOUT once a wait of the 4-bit
+// attention ran out, also when an earlier error holds status[0].
 struct Status {
     int code;
     int detail;

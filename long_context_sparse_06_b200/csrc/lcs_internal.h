@@ -168,5 +168,6 @@ bool encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, 
 
 // Bounded-wait self-test (selftest.cu): one CTA waits on an mbarrier nothing completes.
 cudaError_t launch_selftest_wait(uint64_t budget_ns, int* status, long long* out, cudaStream_t stream);
+cudaError_t launch_selftest_warp_wait(uint64_t delay_ns, int* status, long long* out, cudaStream_t stream);   // attend_kv4.cu
 
 }  // namespace lcs
