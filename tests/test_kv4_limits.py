@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_kv4 import DEV, G, L, gpu   # noqa: F401 (fixtures)
+from test_kv4 import BF, DEV, G, L, case, gpu   # noqa: F401 (fixtures)
 
 
 def test_selftest_warp_wait_rejects_bad_arguments_without_device(L):
@@ -32,3 +32,16 @@ def test_waits_outlast_another_requests_error(G, code, gave_up, held):
     assert ws[:4].view(torch.int32).item() == code           # what was recorded stays
     assert G.lcs_status(ws) == code and G.lcs_status(ws) == 0
     assert (ws == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("d_c,d_r,dt", [(512, 64, BF), (64, 16, torch.float32)])
+@pytest.mark.parametrize("op", ["csa", "hca"])
+def test_window_positions_of_any_size(G, op, d_c, d_r, dt):
+    """A query before the window's first row sees none of it and one far past it none either, also where the
+    difference of the two positions passes 64 bits (it must not wrap to a small one)."""
+    top, low = (1 << 63) - 1, -(1 << 63)
+    win0 = [top, low, top - 1, 0]
+    pos = [[low, low + 1, top, -1], [top, top - 1, low, low + 3], [low, low + 20, top, 5], [low, top, 7, -1]]
+    case(G, op, 4, 30, 4, 8, d_c, d_r, dt, Tw=20, k=9, Q=4, q_pos=pos, win_pos0=win0, m=3, W=6, seed=1)
+    case(G, op, 4, 0, 4, 8, d_c, d_r, dt, Tw=1, k=9, Q=4, q_pos=pos, win_pos0=win0, m=3, W=1, seed=2)
