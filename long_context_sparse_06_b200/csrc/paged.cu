@@ -28,6 +28,7 @@ namespace {
 // neighbouring slots a thread, each looked up by itself), half of it the scan and the launch.
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxB = 8192;
+constexpr int64_t kPlanFar = int64_t(1) << 52;   // tokens
 
 // Quotient of a length: nearly always of 32 bits, where the division is several times cheaper.
 __device__ __forceinline__ int64_t plan_div(int64_t a, int b) {
@@ -43,10 +44,10 @@ __device__ __forceinline__ PlanReq plan_req(const int64_t* len, const int64_t* n
     r.n = n_new[b];
     if (r.len < 0) r.n = 0, r.len = 0;
     if (r.n < 0) r.n = 0;
-    // lengths past 2^40 tokens cannot be held by any table: the check against max_blocks
-    // refuses them, and the clamp keeps the sums below from wrapping
-    if (r.len > (int64_t(1) << 40)) r.len = int64_t(1) << 40;
-    if (r.n > (int64_t(1) << 40)) r.n = int64_t(1) << 40;
+    // a table holds less than 2^31 blocks of at most 2^20 tokens: the check against max_blocks refuses what
+    // is clamped here, and len + n does not wrap
+    if (r.len > kPlanFar) r.len = kPlanFar;
+    if (r.n > kPlanFar) r.n = kPlanFar;
     return r;
 }
 
@@ -92,6 +93,9 @@ __global__ void __launch_bounds__(kPlanThreads)
             v[1] = plan_div(r.len + r.n, o0.m) - plan_div(r.len, o0.m);
             v[2] = o1.m > 0 ? plan_div(r.len + r.n, m1) - plan_div(r.len, m1) : 0;
             if (r.n > 0 && nb1 > max_blocks) bad_s = 1;
+            // (a count from 2^31 on is refused below by itself; cut there, 8192 of them add up without a wrap)
+#pragma unroll
+            for (int i = 0; i < 3; ++i) v[i] = v[i] < (int64_t(1) << 32) ? v[i] : int64_t(1) << 32;
         }
         int64_t x[3];
 #pragma unroll

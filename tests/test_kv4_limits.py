@@ -45,3 +45,33 @@ def test_window_positions_of_any_size(G, op, d_c, d_r, dt):
     pos = [[low, low + 1, top, -1], [top, top - 1, low, low + 3], [low, low + 20, top, 5], [low, top, 7, -1]]
     case(G, op, 4, 30, 4, 8, d_c, d_r, dt, Tw=20, k=9, Q=4, q_pos=pos, win_pos0=win0, m=3, W=6, seed=1)
     case(G, op, 4, 0, 4, 8, d_c, d_r, dt, Tw=1, k=9, Q=4, q_pos=pos, win_pos0=win0, m=3, W=1, seed=2)
+
+
+@gpu
+def test_page_plan_of_long_requests(G):
+    """Tables of large blocks hold more than 2^40 tokens: block and slot of the entry that completes are those of
+    the length itself; lengths that no table holds are refused, whatever their size."""
+    P, wide = 1 << 20, (1 << 21) + 3
+    lens = torch.tensor([1 << 41, 5, (1 << 40) + P, 1 << 60], device=DEV)
+    new = torch.tensor([P, P, 3 * P, 0], device=DEV)
+    free = torch.arange(90, 100, dtype=torch.int32, device=DEV)
+    table = torch.full((4, wide), -9, dtype=torch.int32, device=DEV)
+    table[1, 0] = 7
+    ws = G.workspace(256)
+    slots, off, slots2, off2, taken = G.lcs_page_plan(lens, new, free, table, block_tokens=P, m=P // 2, max_slots=20, m2=P,
+                                                      max_slots2=9, ws=ws)
+    assert G.lcs_status(ws) == 0
+    want = torch.full((4, wide), -9, dtype=torch.int32)
+    want[0, 1 << 21] = 90
+    want[1, 0], want[1, 1] = 7, 91
+    want[2, (1 << 20) + 1:(1 << 20) + 4] = torch.tensor([92, 93, 94], dtype=torch.int32)
+    assert torch.equal(table.cpu(), want) and taken.item() == 5
+    assert off.tolist() == [0, 2, 4, 10, 10] and off2.tolist() == [0, 1, 2, 5, 5]
+    # request 1 completes half-block entries 0, 1 of block 7; the others fill whole new blocks
+    assert slots.tolist() == [180, 181, 14, 15, 184, 185, 186, 187, 188, 189] + [-1] * 10
+    assert slots2.tolist() == [90, 7, 92, 93, 94] + [-1] * 4
+    for n, a in (((1 << 41) + 3 * P, 1), (1 << 62, 1), ((1 << 63) - 1, (1 << 63) - 1), (0, (1 << 63) - 1), (0, 1 << 52), (1 << 45, 1 << 41)):
+        t = want.to(DEV)
+        out = G.lcs_page_plan(torch.tensor([0, n] * 20, device=DEV), torch.tensor([0, a] * 20, device=DEV), free,
+                              t[:1].repeat(40, 1), block_tokens=P, m=1, max_slots=20, ws=ws)
+        assert G.lcs_status(ws) == -5 and out[4].item() == 0 and (out[0] == -1).all() and (out[1] == 0).all(), (n, a)
