@@ -385,7 +385,8 @@ LCS_API int lcs_kv4_load(const void* pool, int64_t n_slots, const int64_t* slots
  *   HCA: every entry of the request (decode), or those below (q_pos + 1) / m.
  *   q_pos [B, Q], win_pos0 [B], W: as csa_attend; both NULL for decode (Q = 1)
  *   out  [B, Q, H, d_c]  LCS_F32 or LCS_BF16;  lse [B, Q, H] fp32 or NULL
- * V is the d_c content dims.  A query that sees no row gives o = 0 and lse = -inf.  Only
+ * V is the d_c content dims.  A query that sees no row gives o = 0 and lse = -inf; a head whose
+ * query holds a NaN gives NaN in both.  Only
  * blocks of rows that are attended are looked up: table entries behind a request's last
  * block and rows behind its last entry may hold anything.  A block id outside [0, n_blocks)
  * records LCS_ERR_DEVICE and leaves that query's output unspecified; n_entries past

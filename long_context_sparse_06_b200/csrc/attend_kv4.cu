@@ -330,12 +330,12 @@ __global__ void __launch_bounds__(256, kPass == 1 ? 4 : 1) attend_kv4_kernel(con
     float* base = qs + kSHeads * pitch;
     const int in_ml = kSRows * pitch + kSRows * kSHeads;   // of a warp's floats
     auto out_at = [&](int h, int c, float4 o, float M, float L) {
-        const float iv = L > 0.f ? 1.f / L : 0.f;
+        const float iv = L != 0.f ? 1.f / L : 0.f;   // (L is 0 where no row was seen; a NaN stays one)
         o = scale4(o, iv);
         const int64_t at = (g * a.H + h0 + h) * a.d_c + 4 * c;
         if (a.out_dtype == LCS_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = o;
         else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(cvt_bf16x2(o.x, o.y), cvt_bf16x2(o.z, o.w));
-        if (c == 0 && a.lse != nullptr) a.lse[g * a.H + h0 + h] = L > 0.f ? M + logf(L) : -INFINITY;
+        if (c == 0 && a.lse != nullptr) a.lse[g * a.H + h0 + h] = L != 0.f ? M + logf(L) : -INFINITY;
     };
     for (int j = t; j < nh * c4n; j += blockDim.x) {
         const int h = j / c4n, c = j - h * c4n;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(256, kPass == 1 ? 4 : 1) attend_kv4_kernel(con
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = 0; w < nw; ++w) {
             const float* x = base + w * wf;
-            const float lw = x[in_ml + kSHeads + h], f = lw > 0.f ? expf(x[in_ml + h] - M) : 0.f;
+            const float lw = x[in_ml + kSHeads + h], f = lw != 0.f ? expf(x[in_ml + h] - M) : 0.f;
             L = fmaf(lw, f, L);
             o = axpy4(f, *reinterpret_cast<const float4*>(x + h * a.d_c + 4 * c), o);
         }
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(256, kPass == 1 ? 4 : 1) attend_kv4_kernel(con
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s = 0; s < splits; ++s) {
             const float ls = ld_dsmem_f32(dsmem_addr(&joint[1][h], s));
-            const float f = ls > 0.f ? expf(ld_dsmem_f32(dsmem_addr(&joint[0][h], s)) - M) : 0.f;
+            const float f = ls != 0.f ? expf(ld_dsmem_f32(dsmem_addr(&joint[0][h], s)) - M) : 0.f;
             L = fmaf(ls, f, L);
             o = axpy4(f, ld_dsmem_f4(dsmem_addr(base + h * a.d_c + 4 * c, s)), o);
         }
@@ -700,14 +700,14 @@ __device__ __forceinline__ void merge_task(const AttendKv4Args& a, int tiles, in
         float m = M;
 #pragma unroll
         for (int k = 0; k < S; ++k) m = fmaxf(m, x[k].x);
-        const float f = L > 0.f ? exp2f(M - m) : 0.f;
+        const float f = L != 0.f ? exp2f(M - m) : 0.f;
         M = m;
         L *= f;
 #pragma unroll
         for (int r = 0; r < R; ++r) acc[r] = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
 #pragma unroll
         for (int k = 0; k < S; ++k) {
-            const float e = s0 + k < splits && x[k].y > 0.f ? exp2f(x[k].x - m) : 0.f;   // no rows, no weight
+            const float e = s0 + k < splits && x[k].y != 0.f ? exp2f(x[k].x - m) : 0.f;   // no rows, no weight
             L += x[k].y * e;
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -716,7 +716,7 @@ __device__ __forceinline__ void merge_task(const AttendKv4Args& a, int tiles, in
         }
     }
     if (head >= a.H) return;
-    const float iv = L > 0.f ? 1.f / L : 0.f;
+    const float iv = L != 0.f ? 1.f / L : 0.f;   // (a NaN stays one)
     const int64_t at = ((int64_t)g * a.H + head) * kDv + (lane < 16 ? 0 : 256) + 4 * j0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -725,7 +725,7 @@ __device__ __forceinline__ void merge_task(const AttendKv4Args& a, int tiles, in
         else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + 4 * r) = make_uint2(cvt_bf16x2(o.x, o.y), cvt_bf16x2(o.z, o.w));
     }
     if (a.lse != nullptr && j0 == 0 && lane < 16)
-        a.lse[(int64_t)g * a.H + head] = L > 0.f ? (M + log2f(L)) / kLog2e : -INFINITY;
+        a.lse[(int64_t)g * a.H + head] = L != 0.f ? (M + log2f(L)) / kLog2e : -INFINITY;
 }
 
 // kCsa: a selection (else every entry).  kJoin: the splits of a unit are a cluster and merge in it.  (Four
@@ -1174,11 +1174,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (nch > 0) warp_wait(&bars.odone, 0, status, 622);
         if (lane < 16) {
-            const float m = l_sum > 0.f ? m_used - kLift : -INFINITY;
-            bars.inv_l[head] = l_sum > 0.f ? 1.f / l_sum : 0.f;
+            const float m = l_sum != 0.f ? m_used - kLift : -INFINITY;   // (0: no row seen; a NaN stays one)
+            bars.inv_l[head] = l_sum != 0.f ? 1.f / l_sum : 0.f;
             if (only) {
                 if (a.lse != nullptr && head < nh)
-                    a.lse[(int64_t)g * a.H + h0 + head] = l_sum > 0.f ? (m + log2f(l_sum)) / kLog2e : -INFINITY;
+                    a.lse[(int64_t)g * a.H + h0 + head] = l_sum != 0.f ? (m + log2f(l_sum)) / kLog2e : -INFINITY;
             } else {
                 float* ml = part_ml + ((int64_t)(unit * splits + sp) * kH + head) * 2;
                 ml[0] = m;

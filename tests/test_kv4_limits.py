@@ -1,8 +1,10 @@
 """The paged 4-bit cache at the limits of what its calls may meet.  References and tolerances are test_kv4's."""
+import math
+
 import pytest
 import torch
 
-from test_kv4 import BF, DEV, G, L, case, gpu   # noqa: F401 (fixtures)
+from test_kv4 import BF, DEV, G, L, case, gen, gpu, make_pool   # noqa: F401 (fixtures)
 
 
 def test_selftest_warp_wait_rejects_bad_arguments_without_device(L):
@@ -75,3 +77,30 @@ def test_page_plan_of_long_requests(G):
         out = G.lcs_page_plan(torch.tensor([0, n] * 20, device=DEV), torch.tensor([0, a] * 20, device=DEV), free,
                               t[:1].repeat(40, 1), block_tokens=P, m=1, max_slots=20, ws=ws)
         assert G.lcs_status(ws) == -5 and out[4].item() == 0 and (out[0] == -1).all() and (out[1] == 0).all(), (n, a)
+
+
+@gpu
+@pytest.mark.parametrize("N,Tw", [(20, 20), (300, 0), (2000, 20), (8000, 128)])
+@pytest.mark.parametrize("d_c,d_r,dt", [(512, 64, BF), (64, 16, torch.float32), (512, 64, torch.float32)])
+def test_a_head_that_is_no_number(G, N, Tw, d_c, d_r, dt):
+    """One split, splits merged in their cluster and by a second kernel, CUDA cores: a NaN in a head's query gives that
+    head NaN outputs and a NaN log-sum, not the -inf of a query without rows, and the other heads what they had."""
+    B, H, D, be = 2, 9, d_c + d_r, 16
+    width = -(-N // be)
+    pool = make_pool(G, B * width, be, d_c, d_r, 1)
+    table = torch.arange(B * width, dtype=torch.int32, device=DEV).view(B, width)
+    n = torch.full((B,), N, device=DEV)
+    q = torch.randn((B, 1, H, D), generator=gen(2), device=DEV).to(dt)
+    win = torch.randn((B, Tw, D), generator=gen(3), device=DEV).to(dt) if Tw else None
+    idx = torch.arange(min(N, 1000), dtype=torch.int32, device=DEV).repeat(B, 1, 1).contiguous()
+    bad = q.clone()
+    bad[0, 0, 4, 7] = math.nan          # a content dim
+    bad[1, 0, 0, D - 1] = math.nan      # a RoPE dim
+    hit = torch.zeros((B, 1, H), dtype=torch.bool, device=DEV)
+    hit[0, 0, 4] = hit[1, 0, 0] = True
+    for call in (lambda q: G.hca_attend_kv4(q, pool, table, n, win, D ** -0.5, d_c=d_c, want_lse=True, out_dtype=torch.float32),
+                 lambda q: G.csa_attend_kv4(q, pool, table, n, win, idx, D ** -0.5, d_c=d_c, want_lse=True)):
+        want, wl = call(q)
+        o, lse = call(bad)
+        assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+        assert torch.equal(o[~hit], want[~hit]) and torch.equal(lse[~hit], wl[~hit])
