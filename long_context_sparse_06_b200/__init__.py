@@ -377,6 +377,10 @@ def kv_fp4_row_bytes(d_c=512, d_r=64):
 
 # These calls last about as long as the GPU needs for one of them in a decode step, so their bindings do
 # little else than check the arguments: one test per tensor, the raw stream handle, one allocation.
+#
+# With `ws` a call is asynchronous and lcs_status(ws) tells what its kernels recorded.  Without one there is no
+# status word that outlives the call, and a plan that did not fit looks like a step that needed nothing: the call
+# then waits for its kernels and raises LcsError itself (in a stream capture, where nothing has run yet, it cannot).
 def _arg(t, name, dtype, shape, dev):
     """The address of tensor `t` (the C call sees addresses only), or ValueError."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
@@ -402,8 +406,9 @@ def _on(stream, t):
     return _torch().cuda.stream(stream)
 
 
-def _call_on(dev, name, *args):
-    """The call on device `dev`: with it current, on its current stream."""
+def _call_on(dev, name, own_ws, *args):
+    """The call on device `dev`: with it current, on its current stream.  own_ws: the workspace that the binding made
+    for this call, whose status word nobody else can read, or None."""
     torch = _torch()
     fn = _fns.get(name)
     if fn is None:
@@ -414,17 +419,22 @@ def _call_on(dev, name, *args):
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, s)
+    if rc == 0 and own_ws is not None:
+        with torch.cuda.device(dev):
+            if not torch.cuda.is_current_stream_capturing():
+                rc = int(own_ws[:4].view(torch.int32))
     if rc != 0:
         raise LcsError(name, rc)
 
 
 def _ws(ws, nbytes, dev):
-    """(address, bytes) of the workspace given, or of a new one of nbytes()."""
+    """(address, bytes, None) of the workspace given, or those of a new one of nbytes() and that one."""
     if ws is None:
         ws = workspace(nbytes(), f"cuda:{dev}")
-    elif ws.get_device() != dev or not ws.is_contiguous():
+        return ws.data_ptr(), ws.numel(), ws
+    if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"ws: a contiguous tensor on cuda:{dev} expected")
-    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+    return ws.data_ptr(), ws.numel() * ws.element_size(), None
 
 
 def _status_bytes():
@@ -435,7 +445,8 @@ def lcs_page_plan(lens, n_new, free_blocks, block_table, block_tokens=128, m=4, 
                   ws=None, stream=None):
     """lens, n_new [B] int64; free_blocks [n_free] int32; block_table [B, max_blocks] int32, extended in
     place -> (slots [max_slots], offsets [B+1], slots2 [max_slots2], offsets2 [B+1], taken [1]), int64;
-    slots2 and offsets2 are None when m2 is 0."""
+    slots2 and offsets2 are None when m2 is 0.  A plan that does not fit (max_slots counts too) takes nothing:
+    LCS_ERR_DEVICE in the status word of ws, or LcsError without one."""
     if stream is not None:
         with _on(stream, lens):
             return lcs_page_plan(lens, n_new, free_blocks, block_table, block_tokens, m, max_slots, m2, max_slots2, ws)
@@ -446,21 +457,21 @@ def lcs_page_plan(lens, n_new, free_blocks, block_table, block_tokens=128, m=4, 
     head = (B, _arg(lens, "lens", i64, (B,), dev), _arg(n_new, "n_new", i64, (B,), dev), block_tokens,
             _arg(free_blocks, "free_blocks", i32, (n_free,), dev), n_free,
             _arg(block_table, "block_table", i32, (B, max_blocks), dev), max_blocks)
-    wp, wb, ws = _ws(ws, _status_bytes, dev)
+    wp, wb, own_ws = _ws(ws, _status_bytes, dev)
     if m2:
         out = lens.new_empty(max_slots + max_slots2 + 2 * B + 3)
         slots, slots2, off, off2, taken = out.split_with_sizes((max_slots, max_slots2, B + 1, B + 1, 1))
         p = out.data_ptr()
         p2 = p + 8 * max_slots
         po = p2 + 8 * max_slots2
-        _call_on(dev, "lcs_page_plan", *head, m, p, max_slots, po, m2, p2, max_slots2, po + 8 * (B + 1),
+        _call_on(dev, "lcs_page_plan", own_ws, *head, m, p, max_slots, po, m2, p2, max_slots2, po + 8 * (B + 1),
                  po + 16 * (B + 1), wp, wb)
         return slots, off, slots2, off2, taken
     out = lens.new_empty(max_slots + B + 2)
     slots, off, taken = out.split_with_sizes((max_slots, B + 1, 1))
     p = out.data_ptr()
     po = p + 8 * max_slots
-    _call_on(dev, "lcs_page_plan", *head, m, p, max_slots, po, 0, None, 0, None, po + 8 * (B + 1), wp, wb)
+    _call_on(dev, "lcs_page_plan", own_ws, *head, m, p, max_slots, po, 0, None, 0, None, po + 8 * (B + 1), wp, wb)
     return slots, off, None, None, taken
 
 
@@ -478,8 +489,8 @@ def lcs_kv4_store(x, slots, pool, d_c=512, ws=None, stream=None):
     dev = _dev(x)
     n, D = x.shape
     pp, n_slots = _pool_arg(pool, d_c, D - d_c, dev)
-    wp, wb, ws = _ws(ws, _status_bytes, dev)
-    _call_on(dev, "lcs_kv4_store", _arg(x, "x", x.dtype, (n, D), dev), _dt(x), n, d_c, D - d_c,
+    wp, wb, own_ws = _ws(ws, _status_bytes, dev)
+    _call_on(dev, "lcs_kv4_store", own_ws, _arg(x, "x", x.dtype, (n, D), dev), _dt(x), n, d_c, D - d_c,
              _arg(slots, "slots", _torch().int64, (n,), dev), pp, n_slots, wp, wb)
     return pool
 
@@ -495,8 +506,8 @@ def lcs_kv4_load(pool, slots, d_c=512, d_r=64, out_dtype=None, out=None, ws=None
     pp, n_slots = _pool_arg(pool, d_c, d_r, dev)
     if out is None:
         out = pool.new_empty((n, d_c + d_r), dtype=out_dtype or torch.bfloat16)
-    wp, wb, ws = _ws(ws, _status_bytes, dev)
-    _call_on(dev, "lcs_kv4_load", pp, n_slots, _arg(slots, "slots", torch.int64, (n,), dev), n, d_c, d_r,
+    wp, wb, own_ws = _ws(ws, _status_bytes, dev)
+    _call_on(dev, "lcs_kv4_load", own_ws, pp, n_slots, _arg(slots, "slots", torch.int64, (n,), dev), n, d_c, d_r,
              _arg(out, "out", out_dtype or out.dtype, (n, d_c + d_r), dev), _dt(out), wp, wb)
     return out
 
@@ -515,7 +526,7 @@ def _attend_kv4(name, q, pool, block_table, n_entries, win, idx, k, hca_m, scale
     Tw = 0 if win is None else win.shape[1]
     out = q.new_empty((B, Q, H, d_c), dtype=out_dtype or dt)
     lse = q.new_empty((B, Q, H), dtype=torch.float32) if want_lse else None
-    wp, wb, ws = _ws(ws, lambda: lcs_workspace_size(OP_ATTEND_KV4, B, Q, max_blocks * be, Tw, k, H, d_c), dev)
+    wp, wb, own_ws = _ws(ws, lambda: lcs_workspace_size(OP_ATTEND_KV4, B, Q, max_blocks * be, Tw, k, H, d_c), dev)
     bf16 = torch.bfloat16
     head = (_arg(q, "q", dt, (B, Q, H, D), dev), BF16 if dt is bf16 else _dt(q),
             _arg(pool, "pool", torch.uint8, (n_blocks, be, kv_fp4_row_bytes(d_c, D - d_c)), dev), n_blocks, be,
@@ -527,9 +538,9 @@ def _attend_kv4(name, q, pool, block_table, n_entries, win, idx, k, hca_m, scale
             *(() if hca_m is None else (hca_m,)), W, H, d_c, D - d_c, scale, out.data_ptr(), BF16 if out.dtype is bf16 else _dt(out),
             None if lse is None else lse.data_ptr(), wp, wb)
     if hca_m is None:
-        _call_on(dev, name, *head, _arg(idx, "idx", torch.int32, (B, Q, k), dev), k, *tail)
+        _call_on(dev, name, own_ws, *head, _arg(idx, "idx", torch.int32, (B, Q, k), dev), k, *tail)
     else:
-        _call_on(dev, name, *head, *tail)
+        _call_on(dev, name, own_ws, *head, *tail)
     return (out, lse) if want_lse else out
 
 

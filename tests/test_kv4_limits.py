@@ -104,3 +104,50 @@ def test_a_head_that_is_no_number(G, N, Tw, d_c, d_r, dt):
         o, lse = call(bad)
         assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
         assert torch.equal(o[~hit], want[~hit]) and torch.equal(lse[~hit], wl[~hit])
+
+
+@gpu
+def test_errors_of_calls_without_a_workspace(G):
+    """Without a workspace there is no status word to read later: the call itself raises what its kernels recorded."""
+    i32 = torch.int32
+    z = lambda v, dt=torch.int64: torch.tensor(v, dtype=dt, device=DEV)
+    pool = make_pool(G, 8, 16, 512, 64, 0)
+    table = torch.arange(8, dtype=i32, device=DEV).view(2, 4)
+    n = z([60, 60])
+    q = torch.randn((2, 1, 8, 576), generator=gen(1), device=DEV).to(BF)
+    win = torch.randn((2, 20, 576), generator=gen(2), device=DEV).to(BF)
+    big, bad = win.clone(), table.clone()
+    big[1, 3, 5] = 2.0 ** 17
+    bad[0, 1] = 8
+    idx = torch.full((2, 1, 4), 60, dtype=i32, device=DEV)
+    x = torch.randn((2, 576), generator=gen(3), device=DEV)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for kw in ({}, {"stream": st}):
+        for call in (lambda: G.lcs_page_plan(z([0]), z([300]), z([1, 2, 3], i32), z([[0, 0, 0]], i32), max_slots=74, **kw),
+                     lambda: G.lcs_page_plan(z([3]), z([1]), z([1], i32), z([[0]], i32), **kw),
+                     lambda: G.lcs_kv4_store(x, z([0, 128]), pool.clone(), **kw),
+                     lambda: G.lcs_kv4_load(pool, z([128, 3]), **kw),
+                     lambda: G.hca_attend_kv4(q, pool, bad, n, win, 0.1, **kw),
+                     lambda: G.hca_attend_kv4(q, pool, table, z([60, 65]), win, 0.1, **kw),
+                     lambda: G.hca_attend_kv4(q, pool, table, n, big, 0.1, **kw),
+                     lambda: G.hca_attend_kv4(q.float(), pool, bad, n, win.float(), 0.1, **kw),
+                     lambda: G.csa_attend_kv4(q, pool, table, n, win, idx, 0.1, **kw)):
+            torch.cuda.synchronize()
+            with pytest.raises(G.LcsError) as e:
+                call()
+            assert e.value.code == -5
+    # the calls that are right, and those with a workspace, raise nothing
+    slots, off, _, _, taken = G.lcs_page_plan(z([0]), z([300]), z([1, 2, 3], i32), z([[0, 0, 0]], i32), max_slots=75)
+    assert taken.item() == 3 and off.tolist() == [0, 75]
+    want = G.hca_attend_kv4(q, pool, table, n, win, 0.1)
+    ws = G.workspace(G.lcs_workspace_size(G.OP_ATTEND_KV4, 2, 1, 64, 20, 0, 8))
+    G.hca_attend_kv4(q, pool, bad, n, win, 0.1, ws=ws)
+    assert G.lcs_status(ws) == -5
+    # a captured call cannot wait for its kernels
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = G.hca_attend_kv4(q, pool, table, n, win, 0.1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
