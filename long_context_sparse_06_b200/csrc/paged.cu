@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         const int sh = (per & (per - 1)) == 0 ? 31 - __clz((int)per) : -1;
         for (int64_t j0 = ((int64_t)blockIdx.x * kPlanThreads + (t - lane32)) * kPlanRun; j0 < n_out;
              j0 += (int64_t)gridDim.x * kPlanThreads * kPlanRun) {
-            const int i0 = (int)j0 + lane32;
+            const int i0 = (int)j0 + lane32;   // (j0 is a multiple of 32 kPlanRun: i0 + 32 k ends at 2^31 - 1)
             int b = -1, end = 0;             // the request at hand and the end of its slots
             uint32_t first = 0;              // position of slot i0 counted from the first block of b's new entries
             const int32_t *held = nullptr, *got = nullptr;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                 const int i = i0 + 32 * k;
                 src[k] = nullptr;
                 r[k] = 0;
-                if (i >= n_slot || i < 0) continue;   // (i < 0: past 2^31)
+                if (i >= n_slot) continue;
                 if (i >= end) {
                     if (b < 0) b = plan_find(of, B, i);
                     else
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 #pragma unroll
             for (int k = 0; k < kPlanRun; ++k) {
                 const int i = i0 + 32 * k;
-                if (i >= 0 && i < n_out) o.slots[i] = id[k] < 0 ? -1 : (int64_t)id[k] * per + r[k];
+                if (i < n_out) o.slots[i] = id[k] < 0 ? -1 : (int64_t)id[k] * per + r[k];
             }
         }
     }

@@ -151,3 +151,19 @@ def test_errors_of_calls_without_a_workspace(G):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, want)
+
+
+@gpu
+def test_page_plan_with_the_most_slots(G):
+    """max_slots up to 2^31 - 1: the last turn's slot indexes end there; every slot behind the last entry is -1."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    z = lambda v, dt=torch.int64: torch.tensor(v, dtype=dt, device=DEV)
+    for most in ((1 << 31) - 1, (1 << 31) - 98):
+        table, ws = torch.full((2, 5), -1, dtype=torch.int32, device=DEV), G.workspace(256)
+        slots, off, _, _, taken = G.lcs_page_plan(z([0, 7]), z([300, 90]), z([4, 1, 3, 9], torch.int32), table, max_slots=most, ws=ws)
+        assert G.lcs_status(ws) == 0 and taken.item() == 3 and off.tolist() == [0, 75, 98]
+        # request 1 holds its first block's first entry: that block is its own table's entry 0, which is -1 here
+        assert slots[:75].tolist() == [b * 32 + j for b in (4, 1, 3) for j in range(32)][:75]
+        assert all((part == -1).all() for part in slots[75:].split(1 << 28))
+        del slots, off, taken
