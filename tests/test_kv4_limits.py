@@ -167,3 +167,37 @@ def test_page_plan_with_the_most_slots(G):
         assert slots[:75].tolist() == [b * 32 + j for b in (4, 1, 3) for j in range(32)][:75]
         assert all((part == -1).all() for part in slots[75:].split(1 << 28))
         del slots, off, taken
+
+
+@gpu
+def test_values_on_a_second_device(G):
+    """After the same calls on device 0, device 1 gives the same bytes: a plan, stored and loaded rows, attention with one
+    split, splits in clusters, splits merged by a kernel, and on CUDA cores with opted-in shared memory."""
+    if torch.cuda.device_count() < 2:
+        pytest.skip("needs two devices")
+
+    def all_calls(dev):
+        g = torch.Generator("cpu").manual_seed(1)
+        r = lambda *s: torch.randn(s, generator=g).to(dev)
+        i = lambda v, dt=torch.int64: torch.tensor(v, dtype=dt, device=dev)
+        ws = G.workspace(1 << 26, dev)
+        table = i([[-1] * 700], torch.int32)
+        out = list(G.lcs_page_plan(i([0]), i([700 * 16]), torch.arange(700, dtype=torch.int32, device=dev), table, block_tokens=16, m=1,
+                                   max_slots=700 * 16, ws=ws)[:2]) + [table]
+        slots = out[0]
+        pool = torch.zeros((700, 16, 400), dtype=torch.uint8, device=dev)
+        G.lcs_kv4_store(r(700 * 16, 576), slots, pool, ws=ws)
+        out += [pool, G.lcs_kv4_load(pool, slots, ws=ws)]
+        q, win, idx = r(1, 1, 64, 576).to(BF), r(1, 128, 576).to(BF), torch.arange(0, 900, 3, dtype=torch.int32, device=dev).view(1, 1, 300)
+        for n, width in ((20, 2), (300, 20), (11200, 700)):
+            t = table[:, :width].contiguous()
+            out += G.hca_attend_kv4(q, pool, t, i([n]), win, 1 / 24, want_lse=True, ws=ws)
+            out += G.hca_attend_kv4(q.float(), pool, t, i([n]), win.float(), 1 / 24, want_lse=True, ws=ws)
+        out += G.csa_attend_kv4(q, pool, table, i([11200]), win, idx, 1 / 24, want_lse=True, ws=ws)
+        st = int(ws[:4].view(torch.int32))
+        return [o.cpu() for o in out] + [torch.tensor(st)]
+
+    first, second = all_calls(torch.device("cuda", 0)), all_calls(torch.device("cuda", 1))
+    assert first[-1] == 0 and second[-1] == 0
+    for a, b in zip(first, second):
+        assert torch.equal(a, b)
