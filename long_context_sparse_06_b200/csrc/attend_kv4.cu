@@ -75,14 +75,15 @@ struct Kv4Window {
 __device__ __forceinline__ Kv4Window kv4_window(const AttendKv4Args& a, const Kv4Query& x) {
     Kv4Window w{0, x.win < 0 ? 0 : (x.win < a.Tw ? x.win : a.Tw)};
     if (a.q_pos == nullptr) return w;
-    // the query's own row, counted from the window's first: the difference of any two positions in order fits in
-    // 64 bits without a sign, and from 2^62 on the window's last row is out of reach (W and Tw are below 2^31)
-    const uint64_t own = (uint64_t)x.pos - (uint64_t)x.win;
-    int64_t hi = own < (1ull << 62) ? (int64_t)own : int64_t(1) << 62, lo = hi - a.W + 1;
+    // the query's own row, counted from the window's first: none if it lies before that, or so far past it that the
+    // difference takes the 64th bit
+    int64_t hi = x.pos < x.win ? -1 : (int64_t)((uint64_t)x.pos - (uint64_t)x.win);
+    int64_t lo = hi < 0 ? 0 : hi - a.W + 1;
     if (lo < 0) lo = 0;
     if (hi > a.Tw - 1) hi = a.Tw - 1;
-    if (x.pos < x.win || hi < lo) return Kv4Window{0, 0};
-    return Kv4Window{lo, hi - lo + 1};
+    w.lo = lo;
+    w.n = hi >= lo ? hi - lo + 1 : 0;
+    return w;
 }
 
 // Row of entry e (0 <= e < kv4_entries) of request b, or null when its block is not one of the
