@@ -64,8 +64,9 @@ extern "C" {
                          §4: the indexer's QK path is FP4).  A tensor of n vectors of length d
                          is two planes: n*d/2 packed bytes (element 2j in the low nibble of
                          byte j), then n*d/32 scale bytes. */
-#define LCS_KV_FP4 4  /* 4-bit KV row ("DeepSeek V4 深度解析" §4, FP4; RoPE dims BF16 as in §2): for
-                         d_c content dims and d_r RoPE dims one row is d_c/2 bytes of E2M1 codes
+#define LCS_KV_FP4 4  /* 4-bit KV row: the format that "DeepSeek V4 深度解析" §4 has for the indexer's QK
+                         path, here for KV content (the page keeps that in FP8), RoPE dims BF16 as
+                         in §2.  For d_c content dims and d_r RoPE dims one row is d_c/2 bytes of E2M1 codes
                          (element 2j in the low nibble of byte j) | d_r bf16 | d_c/32 E4M3 scales,
                          scale b applying to content dims [32b, 32b+32), zero-padded to a multiple
                          of 16 bytes.  d_c = 512, d_r = 64: 400 bytes.  The type of the paged pool
@@ -326,8 +327,8 @@ LCS_API int lcs_cache_append(int64_t B, const int64_t* pos, const void* x, const
                  int kv_dtype, int kI_dtype, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
- * The compressed cache in pages and 4 bits ("DeepSeek V4 深度解析" §4, KV-cache management:
- * the compressed entries lie in blocks, each covering lcm(4, 128) raw tokens; FP4).  A pool
+ * The compressed cache in pages ("DeepSeek V4 深度解析" §4, KV-cache management: the compressed
+ * entries lie in blocks, each covering lcm(4, 128) raw tokens) and in LCS_KV_FP4 rows.  A pool
  * holds n_blocks blocks of block_entries rows each; block_table[b][i] is the block of
  * request b's entries [i*block_entries, (i+1)*block_entries), so entry e lies in slot
  * block_table[b][e / block_entries] * block_entries + e % block_entries.  With blocks of 128
@@ -386,16 +387,19 @@ LCS_API int lcs_kv4_load(const void* pool, int64_t n_slots, const int64_t* slots
  *   q_pos [B, Q], win_pos0 [B], W: as csa_attend; both NULL for decode (Q = 1)
  *   out  [B, Q, H, d_c]  LCS_F32 or LCS_BF16;  lse [B, Q, H] fp32 or NULL
  * V is the d_c content dims.  A query that sees no row gives o = 0 and lse = -inf; a head whose
- * query holds a NaN gives NaN in both.  Only
- * blocks of rows that are attended are looked up: table entries behind a request's last
- * block and rows behind its last entry may hold anything.  A block id outside [0, n_blocks)
- * records LCS_ERR_DEVICE and leaves that query's output unspecified; n_entries past
- * max_blocks * block_entries records it too and counts as that.
+ * query holds a NaN gives NaN in both.  Table entries behind a request's last block and rows
+ * behind its last entry may hold anything: they may be read ahead of time, but count for
+ * nothing.  An attended block whose id is outside [0, n_blocks) records LCS_ERR_DEVICE and
+ * leaves that query's output unspecified; n_entries past max_blocks * block_entries records it
+ * too and counts as that.
  * d_c, d_r as lcs_kv4_store; d_c = 512, d_r = 64 with bf16 q runs on the tensor cores.  There
  * the content dims and the weights are fp16 operands: stored rows are exact in it; q is scaled
- * by a power of two per head (exact down to 2^-28 of the head's largest element); window
- * content is exact from 2^-14 up, off by at most 2^-25 below, and a magnitude of 2^16 or more
- * records LCS_ERR_DEVICE; a weight is off by at most 2^-11 of itself.  RoPE dims stay bf16: of
+ * by a power of two per head (elements down to 2^-31 of the head's largest are exact, smaller
+ * ones off by at most 2^-39 of it, where the largest is 2^-112 or more); window content is
+ * exact from 2^-17 up, off by at most 2^-25 below, and a magnitude of 2^16 or more records
+ * LCS_ERR_DEVICE; a weight is off by at most 2^-11 of itself or 2^-31 of the largest one,
+ * whichever is more: over R rows the small ones can take up to R * 2^-31 of the largest from
+ * an output's sum (lse has them all).  RoPE dims stay bf16: of
  * magnitude below 2^100, so that fp32 sums hold (on either path |scale q.K| <= 2^23 and
  * finite q and attended rows; other outputs are unspecified).  q, pool, win and out on 16
  * bytes; max_blocks * block_entries + Tw < 2^31 - 2^16.  Workspace: lcs_workspace_size(

@@ -1,7 +1,7 @@
 // attend_kv4.cu -- shared-KV MQA over a paged cache held in 4 bits (CSA sparse; HCA dense).
 //
 // "DeepSeek V4 深度解析" §2, CSA step 3 and HCA paragraph (the attention), §4 (the cache in
-// blocks; FP4).  For query (b,q) and head h, over the compressed rows and the window rows R
+// blocks).  For query (b,q) and head h, over the compressed rows and the window rows R
 // that the query sees:
 //   o_h = sum_r softmax_r(scale * q_h . K_r) V_r,   V_r = the d_c content dims of K_r.
 // A compressed row is stored as E2M1 codes with an E4M3 scale per 32 content dims and bf16
@@ -429,11 +429,11 @@ cudaError_t launch_simt(const AttendKv4Args& a, int* status, cudaStream_t s) {
 //    exact in fp16: one conversion per pair of codes and one fp16 multiply by the scale, half of what
 //    bf16 would take.  Both operands of a kind::f16 MMA have one type, so the content dims of Q are
 //    fp16 too, scaled per head by a power of two that puts the head's largest element in
-//    [2^14, 2^15) (exact down to 2^-28 of it, below that off by 2^-39 of it), and P is fp16 (11
-//    bits; 2^-11 a weight, against 2^-8 of bf16).  RoPE dims stay bf16: four MMAs of the same
-//    accumulation.  Window rows' content goes from bf16 to fp16 as well: exact from 2^-14 to 65504
-//    (their bf16 has 8 bits), off by 2^-25 below, where 4-bit rows resolve 2^-10, and saturating
-//    above, where 4-bit rows end at 2688.
+//    [2^14, 2^15) (8 bits: exact from 2^-17 on, 2^-31 of it, below that off by 2^-25, 2^-39 of it), and
+//    P is fp16 (11 bits; 2^-11 a weight, against 2^-9 of bf16, or 2^-31 of the largest below 2^-20 of
+//    it).  RoPE dims stay bf16: four MMAs of the same accumulation.  Window rows' content goes from
+//    bf16 to fp16 as well: exact from 2^-17 (8 bits) to 65280, off by 2^-25 below, where 4-bit rows
+//    resolve 2^-10; from 2^16 on, where 4-bit rows end at 2688, it is an error.
 //  * Shared memory is what an SM runs out of: its bandwidth (an MMA with both operands in it takes
 //    4 KB per 32 cycles) and its size (a chunk is the K-major B of Q.K^T and the MN-major B of P.V).
 //    So 384 of Q's dims are an A operand in TMEM, in the lanes of the accumulator they meet: S of
@@ -605,7 +605,8 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-// Two bf16 -> two fp16: exact from 2^-14 to 65504, where it saturates; below off by 2^-25 at most.
+// Two bf16 -> two fp16: exact from 2^-17 (8 bits above fp16's last, 2^-24) to 65280, off by at most 2^-25
+// below, saturating above.
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
     uint32_t r;
     asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(w & 0xFFFF0000u)), "f"(__uint_as_float(w << 16)));

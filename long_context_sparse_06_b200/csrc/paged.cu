@@ -2,7 +2,8 @@
 // requests' lengths, and the cache writer and reader of LCS_KV_FP4 rows.
 //
 // "DeepSeek V4 深度解析" §4 keeps the compressed cache in blocks that cover lcm(4, 128)
-// raw tokens; its FP4 paragraph gives the 4-bit format (E2M1 codes, an E4M3 scale per 32).
+// raw tokens; its FP4 paragraph has 4 bits for the indexer's QK path.  The rows here are KV content in
+// that format (E2M1 codes, an E4M3 scale per 32), which the page keeps in FP8: this library's choice.
 #include <type_traits>
 #include <utility>
 

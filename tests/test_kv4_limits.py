@@ -201,3 +201,34 @@ def test_values_on_a_second_device(G):
     assert first[-1] == 0 and second[-1] == 0
     for a, b in zip(first, second):
         assert torch.equal(a, b)
+
+
+@gpu
+def test_small_window_values(G):
+    """One window row alone is the output: content is exact from 2^-17 up and off by at most 2^-25 below."""
+    v = torch.arange(128, 256, device=DEV) * 2.0 ** -24                                  # every bf16 value of [2^-17, 2^-16)
+    small = torch.randint(-255, 256, (256,), generator=gen(1), device=DEV) * 2.0 ** -27
+    win = torch.cat((v, -4 * v, small, torch.zeros(64, device=DEV))).to(BF).view(1, 1, 576)
+    q = torch.randn((1, 1, 64, 576), generator=gen(2), device=DEV).to(BF)
+    z = torch.zeros((1, 1), dtype=torch.int32, device=DEV)
+    o = G.hca_attend_kv4(q, make_pool(G, 1, 1, 512, 64, 3), z, z[0].long(), win, 1 / 24, out_dtype=torch.float32)[0, 0]
+    want = win[0, 0, :512].double()
+    assert torch.equal(o[:, :256].double(), want[:256].expand(64, 256))
+    assert ((o.double() - want).abs() <= 2.0 ** -25).all() and (o[:, 256:] != 0).any()
+
+
+@gpu
+def test_small_weights(G):
+    """Two window rows whose scores lie (h + 1) / 2 apart, content 0 and 1: the output is the second's weight, off by at
+    most 2^-11 of itself or 2^-31 of the first's, and by the 2^-17 of exp2 and its argument; the log-sum has all of it."""
+    win = torch.zeros((1, 2, 576), device=DEV)
+    win[0, 1, :512], win[0, 1, 512] = 1, 1
+    q = torch.zeros((1, 1, 64, 576), device=DEV)
+    q[0, 0, :, 512] = -(torch.arange(64, device=DEV) + 1) / 2
+    z = torch.zeros((1, 1), dtype=torch.int32, device=DEV)
+    o, lse = G.hca_attend_kv4(q.to(BF), make_pool(G, 1, 1, 512, 64, 3), z, z[0].long(), win.to(BF), 1.0, want_lse=True, out_dtype=torch.float32)
+    e = torch.exp(q[0, 0, :, 512].double())
+    p = (e / (1 + e))[:, None]
+    tol = torch.clamp(p * 2.0 ** -11, min=2.0 ** -31) + p * 2.0 ** -17
+    assert ((o[0, 0].double() - p).abs() <= tol).all()
+    assert ((lse[0, 0].double() - torch.log1p(e)).abs() <= 2.0 ** -18).all()
