@@ -386,8 +386,8 @@ LCS_API int lcs_kv4_load(const void* pool, int64_t n_slots, const int64_t* slots
  *   HCA: every entry of the request (decode), or those below (q_pos + 1) / m.
  *   q_pos [B, Q], win_pos0 [B], W: as csa_attend; both NULL for decode (Q = 1)
  *   out  [B, Q, H, d_c]  LCS_F32 or LCS_BF16;  lse [B, Q, H] fp32 or NULL
- * V is the d_c content dims.  A query that sees no row gives o = 0 and lse = -inf; a head whose
- * query holds a NaN gives NaN in both.  Table entries behind a request's last block and rows
+ * V is the d_c content dims.  A query that sees no row gives o = 0 and lse = -inf; over rows, a
+ * head whose query holds a NaN gives NaN in both.  Table entries behind a request's last block and rows
  * behind its last entry may hold anything: they may be read ahead of time, but count for
  * nothing.  An attended block whose id is outside [0, n_blocks) records LCS_ERR_DEVICE and
  * leaves that query's output unspecified; n_entries past max_blocks * block_entries records it
@@ -401,7 +401,7 @@ LCS_API int lcs_kv4_load(const void* pool, int64_t n_slots, const int64_t* slots
  * whichever is more: over R rows the small ones can take up to R * 2^-31 of the largest from
  * an output's sum (lse has them all).  RoPE dims stay bf16: of
  * magnitude below 2^100, so that fp32 sums hold (on either path |scale q.K| <= 2^23 and
- * finite q and attended rows; other outputs are unspecified).  q, pool, win and out on 16
+ * finite q and attended rows; but for NaN queries other outputs are unspecified).  q, pool, win and out on 16
  * bytes; max_blocks * block_entries + Tw < 2^31 - 2^16.  Workspace: lcs_workspace_size(
  * LCS_OP_ATTEND_KV4, B, Q, N_c = max_blocks * block_entries, Tw, k (0 for HCA), H, d_v = d_c, 0),
  * for every W.
